@@ -67,13 +67,16 @@ def strip_comments(src: str) -> str:
 
 SSD_SOURCES = ("kernel_ssd.cuh", "ssd.cu")
 HOST_ONLY_SOURCES = ("host_pipe.cu",)  # copies and sub-plan calls: no kernel launch of its own
+# the recurrent block's other operators, whose kernels no workload here launches
+BLOCK_SOURCES = ("abi_checks.cuh", "column_sums.cuh", "glr.cu", "glr_math.cuh", "kernel_glr.cuh",
+                 "kernel_norm.cuh", "norm.cu")
 
 
 def kernel_sources_hash(read=None, family: str = "scan") -> str:
     """sha256 over the code (comments stripped) of one family of forward kernels and
     their host code, to tell whether a stored ncu figure is current: "scan" (the
-    selective-scan kernels: every CUDA source but the backward's and the SSD form's)
-    or "ssd" (the SSD form's sources and the shared device utilities); the host-buffer
+    selective-scan kernels: every CUDA source but the backward's, the SSD form's and the
+    block operators') or "ssd" (the SSD form's sources and the shared device utilities); the host-buffer
     pipeline's file launches nothing itself and is in neither.  ``read(name)`` returns a
     file's text (default: the working tree)."""
     import hashlib
@@ -84,7 +87,7 @@ def kernel_sources_hash(read=None, family: str = "scan") -> str:
     if family == "ssd":
         names = [n for n in names if n in SSD_SOURCES or n == "device_utils.cuh"]
     else:
-        names = [n for n in names if n not in SSD_SOURCES]
+        names = [n for n in names if n not in SSD_SOURCES and n not in BLOCK_SOURCES]
     for name in names:
         if read is None:
             with open(os.path.join(cdir, name), encoding="utf-8") as f:

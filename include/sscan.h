@@ -271,6 +271,114 @@ SSCAN_API int sscan_ssd_forward(int64_t B, int64_t L, int64_t H, int64_t P, int6
                                 const float *delta, const float *A, const void *B_in, const void *C_in,
                                 const float *h0, void *y, float *h_final, int *status, void *stream);
 
+/* Gated linear recurrence: one state per channel, moved by data-dependent gates (the
+ * recurrence of "tm_ssm_selective", section "Delta is a gate, exactly", with one state a
+ * channel, and its form with a decay rate per channel).  With
+ *     s_t = sigmoid(gate_t),   u_t = sigmoid(input_gate_t) x_t   (no input gate: u_t = x_t)
+ *     rate == NULL:  a_t = s_t,               beta_t = 1 - s_t
+ *     rate given:    a_t = exp(-rate[d] s_t), beta_t = sqrt(1 - a_t^2)
+ * for every batch row b and channel d
+ *     h_t = a_t h_{t-1} + beta_t u_t   (h before t = 0: h0, or 0),   y_t = h_t,
+ *     h_final = h after the last token.
+ * Shape-based (no plan, no workspace):
+ *   B, L, D            batch rows, tokens, channels (B, D >= 1; L >= 0)
+ *   dtype              SSCAN_F32 or SSCAN_BF16: x, the gates and y
+ *   x, gate            [B][L][D]
+ *   input_gate         [B][L][D], or NULL
+ *   rate               [D] fp32, every value > 0, or NULL.  (A rate of 0 holds the state;
+ *                      its gradient is not defined.)
+ *   h0                 [B][D] fp32, or NULL for a zero initial state
+ *   y                  [B][L][D] (output)
+ *   h_final            [B][D] fp32 (output), or NULL; may be the same buffer as h0
+ *   states             sscan_glr_states_bytes(B, L, D) bytes (output), or NULL: states
+ *                      along the sequence that sscan_glr_backward continues from.  Their
+ *                      layout is the library's own.
+ * Gates of +-infinity mean exactly 1 and 0.  A state that is infinite or NaN makes the
+ * later outputs of its channel and batch row infinite or NaN, and no others.
+ * The state and all arithmetic are fp32; sums run in an order that the sizes fix, so equal
+ * calls give equal bits.  Keeps nothing between calls: it may be captured in a CUDA graph.
+ * Every pointer is caller-owned device memory, 16-byte aligned; outputs must not overlap
+ * inputs (but h_final = h0) nor each other.  Asynchronous on `stream`.  Errors as for
+ * sscan_forward. */
+SSCAN_API size_t sscan_glr_states_bytes(int64_t B, int64_t L, int64_t D);
+SSCAN_API int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                                const void *input_gate, const float *rate, const float *h0, void *y,
+                                float *h_final, float *states, void *stream);
+
+/* Backward pass of sscan_glr_forward: with G_t = dy_t + a_{t+1} G_{t+1} (G past the last
+ * token: dh_final, or 0) the gradient of h_t, the chain rule through the formulas above.
+ *   x, gate, input_gate, rate   as passed to the forward
+ *   states             as written by sscan_glr_forward for the same B, L and D
+ *   dy                 [B][L][D], dtype
+ *   dh_final           [B][D] fp32, or NULL (zero)
+ *   dx, dgate          [B][L][D], dtype (output)
+ *   dinput_gate        [B][L][D], dtype (output): given exactly when input_gate is
+ *   drate              [D] fp32 (output, summed over batch and time): given exactly when rate is
+ *   dh0                [B][D] fp32 (output), or NULL to skip it
+ *   workspace          sscan_glr_backward_workspace_bytes(B, L, D) bytes when rate is given
+ *                      (partial sums of drate), else it may be NULL
+ * Ownership, order of sums, graphs, alignment, overlap and errors as for sscan_glr_forward;
+ * calls that may run at the same time need workspaces of their own. */
+SSCAN_API size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D);
+SSCAN_API int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                                 const void *input_gate, const float *rate, const float *states, const void *dy,
+                                 const float *dh_final, void *dx, void *dgate, void *dinput_gate, float *drate,
+                                 float *dh0, void *workspace, void *stream);
+
+/* flags of the norm */
+enum {
+    /* no mean is removed: rstd = 1 / sqrt(mean(s^2) + eps) */
+    SSCAN_NORM_RMS = 1u << 0,
+    /* residual, residual_out, dresidual and ds are fp32 whatever dtype is */
+    SSCAN_NORM_RESIDUAL_F32 = 1u << 1
+};
+
+/* Layer norm over the last axis of [rows][D], after the residual addition of a pre-norm
+ * block (the layer around the recurrences above; no counterpart in the pages):
+ *     s = x + residual, rounded to the residual's type   (no residual: s = x)
+ *     y = (s - mean(s)) rstd weight + bias,   rstd = 1 / sqrt(var(s) + eps)
+ *   rows, D            rows >= 0, D >= 1
+ *   dtype, flags       of x and y: SSCAN_F32 or SSCAN_BF16; any of SSCAN_NORM_*.  The
+ *                      residual has dtype, or fp32 with SSCAN_NORM_RESIDUAL_F32.
+ *   eps                >= 0, added to the variance
+ *   x                  [rows][D]
+ *   residual           [rows][D], or NULL
+ *   weight, bias       [D] fp32, or NULL (1 and 0)
+ *   y                  [rows][D] (output)
+ *   residual_out       [rows][D], the residual's type (output, s): given exactly when residual is
+ *   mean, rstd         [rows] fp32 (output), or NULL; mean must be NULL with SSCAN_NORM_RMS
+ * Sums are fp32 in an order that the sizes fix (variance from centred squares).  No
+ * workspace; nothing is kept between calls, so it may be captured in a CUDA graph.  Every
+ * pointer is caller-owned device memory, 16-byte aligned; outputs must not overlap inputs
+ * nor each other.  Asynchronous on `stream`.  Errors as for sscan_forward. */
+SSCAN_API int sscan_norm_forward(int64_t rows, int64_t D, int dtype, uint32_t flags, float eps, const void *x,
+                                 const void *residual, const float *weight, const float *bias, void *y,
+                                 void *residual_out, float *mean, float *rstd, void *stream);
+
+/* Backward pass of sscan_norm_forward.  With z = (s - mean) rstd:
+ *     ds = rstd (weight dy - mean(weight dy) - z mean(weight dy z)) + dresidual
+ *          (without the middle term with SSCAN_NORM_RMS)
+ *     dweight = sum over rows of dy z,   dbias = sum over rows of dy
+ *   dy                 [rows][D], dtype
+ *   s                  [rows][D]: the forward's residual_out, or its x when it had no residual
+ *                      (then without SSCAN_NORM_RESIDUAL_F32)
+ *   mean, rstd         as written by the forward (mean NULL with SSCAN_NORM_RMS)
+ *   weight             as passed to the forward, or NULL
+ *   dresidual          [rows][D], the type of s: the gradient that reaches residual_out from
+ *                      its other uses, or NULL
+ *   ds                 [rows][D], the type of s (output): the gradient of x and of residual
+ *   dx                 [rows][D], dtype (output), or NULL: ds rounded to dtype; only where the
+ *                      types differ (SSCAN_BF16 with SSCAN_NORM_RESIDUAL_F32)
+ *   dweight, dbias     [D] fp32 (output), or NULL; dweight only with a weight
+ *   workspace          sscan_norm_backward_workspace_bytes(rows, D) bytes when dweight or
+ *                      dbias is given, else it may be NULL
+ * Ownership, order of sums, graphs, alignment, overlap and errors as for sscan_norm_forward;
+ * calls that may run at the same time need workspaces of their own. */
+SSCAN_API size_t sscan_norm_backward_workspace_bytes(int64_t rows, int64_t D);
+SSCAN_API int sscan_norm_backward(int64_t rows, int64_t D, int dtype, uint32_t flags, const void *dy, const void *s,
+                                  const float *mean, const float *rstd, const float *weight, const void *dresidual,
+                                  void *ds, void *dx, float *dweight, float *dbias, void *workspace, void *stream);
+
 /* Wait for `stream`, then read and clear the plan's device status word.
  * Returns SSCAN_OK, SSCAN_ERR_TIMEOUT, or SSCAN_ERR_CUDA. */
 SSCAN_API int sscan_get_status(sscan_plan_t plan, void *stream);

@@ -19,13 +19,16 @@ LIB_PATH = os.path.join(_HERE, "libsscan.so")
 F32, BF16 = 0, 1
 ZOH = 1
 DELTA_SOFTPLUS = 2
+NORM_RMS, NORM_RESIDUAL_F32 = 1, 2
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(7)
 
 SYMBOLS = ("sscan_plan_create", "sscan_plan_destroy", "sscan_workspace_bytes", "sscan_forward",
            "sscan_get_status", "sscan_status_string", "sscan_plan_describe", "sscan_version",
            "sscan_forward_noalloc", "sscan_noalloc_status", "sscan_forward_gated", "sscan_backward",
            "sscan_backward_workspace_bytes", "sscan_ssd_forward", "sscan_backward_gated",
-           "sscan_host_workspace_bytes", "sscan_forward_host")
+           "sscan_host_workspace_bytes", "sscan_forward_host", "sscan_glr_states_bytes", "sscan_glr_forward",
+           "sscan_glr_backward_workspace_bytes", "sscan_glr_backward", "sscan_norm_forward",
+           "sscan_norm_backward_workspace_bytes", "sscan_norm_backward")
 
 
 class SscanError(RuntimeError):
@@ -83,6 +86,20 @@ def lib() -> ctypes.CDLL:
             L.sscan_host_workspace_bytes.restype = sz
             L.sscan_forward_host.argtypes = [vp] * 13
             L.sscan_forward_host.restype = ip
+            L.sscan_glr_states_bytes.argtypes = [i64, i64, i64]
+            L.sscan_glr_states_bytes.restype = sz
+            L.sscan_glr_forward.argtypes = [i64, i64, i64, ip] + [vp] * 9
+            L.sscan_glr_forward.restype = ip
+            L.sscan_glr_backward_workspace_bytes.argtypes = [i64, i64, i64]
+            L.sscan_glr_backward_workspace_bytes.restype = sz
+            L.sscan_glr_backward.argtypes = [i64, i64, i64, ip] + [vp] * 14
+            L.sscan_glr_backward.restype = ip
+            L.sscan_norm_forward.argtypes = [i64, i64, ip, u32, ctypes.c_float] + [vp] * 9
+            L.sscan_norm_forward.restype = ip
+            L.sscan_norm_backward_workspace_bytes.argtypes = [i64, i64]
+            L.sscan_norm_backward_workspace_bytes.restype = sz
+            L.sscan_norm_backward.argtypes = [i64, i64, ip, u32] + [vp] * 12
+            L.sscan_norm_backward.restype = ip
             _lib = L
     return _lib
 
@@ -346,3 +363,263 @@ def ssd_forward(x, delta, A, B, C, h0=None, y=None, h_final=None, want_final: bo
     if rc != OK:
         raise SscanError(rc, "sscan_ssd_forward")
     return y, h_final
+
+
+# --------------------------------------------------------------------------
+# Recurrent block operators: the gated linear recurrence and the layer norm.
+
+def _want(name, t, shape, dt, dev):
+    """Raise unless t is a contiguous CUDA tensor of this shape, dtype and device."""
+    if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous CUDA {dt} {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+class _On:
+    """Context of one call: the tensors' device current, and new tensors allocated on the
+    call's stream (so that the allocator knows who uses them).  Entered only when either
+    differs from what is current."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self._d = torch.cuda.device(self.dev)
+        self._d.__enter__()
+        self._s = torch.cuda.stream(self.stream)
+        self._s.__enter__()
+
+    def __exit__(self, *exc):
+        self._s.__exit__(*exc)
+        self._d.__exit__(*exc)
+
+
+def _on_device(fn, ref, stream, kw):
+    """Run fn(stream pointer, **kw) with ref's device current on ``stream`` (default: that
+    device's current stream)."""
+    if not ref.is_cuda:
+        raise ValueError(f"want CUDA tensors, got one on {ref.device}")
+    dev = ref.device
+    if stream is None:
+        cur = torch.cuda.current_stream(dev)
+        if torch.cuda.current_device() == dev.index:
+            return fn(cur.cuda_stream, **kw)
+        stream = cur
+    elif stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    with _On(dev, stream):
+        return fn(stream.cuda_stream, **kw)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=None, want_final: bool = True,
+                states=None, want_states: bool = False, stream=None):
+    """Gated linear recurrence (``sscan_glr_forward``) on CUDA tensors.
+
+    x, gate and input_gate (or None): [B, L, D] float32 or bfloat16; rate: [D] float32 > 0
+    or None; h0: [B, D] float32 or None.  h_final may be h0 (a decode step in place).
+    ``want_states`` returns the saved states that ``glr_backward`` reads (or pass a buffer
+    of ``new_glr_states`` as ``states``).  Work and new tensors are on ``stream`` (default:
+    the current stream of x's device).
+    Returns (y [B, L, D], h_final [B, D] float32 or None, states or None)."""
+    return _on_device(_glr_forward, x, stream, dict(
+        x=x, gate=gate, rate=rate, input_gate=input_gate, h0=h0, y=y, h_final=h_final, want_final=want_final,
+        states=states, want_states=want_states))
+
+
+def new_glr_states(B: int, L: int, D: int, device="cuda") -> torch.Tensor:
+    """A buffer for the states that ``glr_forward`` saves for ``glr_backward``."""
+    return torch.empty(int(lib().sscan_glr_states_bytes(B, L, D)) // 4, dtype=torch.float32, device=device)
+
+
+def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states):
+    shape, dt, dev = x.shape, x.dtype, x.device
+    code = _dtype_code(dt)
+    if len(shape) != 3:
+        raise ValueError(f"x: want [B, L, D], got {tuple(shape)}")
+    B, L, D = shape
+    _want("x", x, shape, dt, dev)
+    _want("gate", gate, shape, dt, dev)
+    if input_gate is not None:
+        _want("input_gate", input_gate, shape, dt, dev)
+    if rate is not None:
+        _want("rate", rate, (D,), torch.float32, dev)
+    if h0 is not None:
+        _want("h0", h0, (B, D), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _want("y", y, shape, dt, dev)
+    if h_final is not None:
+        _want("h_final", h_final, (B, D), torch.float32, dev)
+    elif want_final:
+        h_final = torch.empty((B, D), dtype=torch.float32, device=dev)
+    if states is not None:
+        _want("states", states, (int(lib().sscan_glr_states_bytes(B, L, D)) // 4,), torch.float32, dev)
+    elif want_states:
+        states = new_glr_states(B, L, D, dev)
+    rc = lib().sscan_glr_forward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0),
+                                 y.data_ptr(), _adr(h_final), _adr(states), st)
+    if rc != OK:
+        raise SscanError(rc, "sscan_glr_forward")
+    return y, h_final, states
+
+
+def glr_backward(x, gate, dy, states, rate=None, input_gate=None, dh_final=None, want_dh0: bool = True,
+                 workspace=None, stream=None) -> dict:
+    """Gradients of ``glr_forward`` (``sscan_glr_backward``): x, gate, rate and input_gate as
+    passed to it, ``states`` as it returned them, dy [B, L, D] and dh_final [B, D] float32
+    (or None).  Returns a dict with dx, dgate and dinput_gate (dtype of x; the last None
+    without an input gate), drate ([D] float32, None without a rate) and dh0 ([B, D]
+    float32, None unless wanted).  ``workspace``: a CUDA uint8 tensor of at least
+    ``sscan_glr_backward_workspace_bytes`` (default: allocated here)."""
+    return _on_device(_glr_backward, x, stream, dict(
+        x=x, gate=gate, dy=dy, states=states, rate=rate, input_gate=input_gate, dh_final=dh_final, want_dh0=want_dh0,
+        workspace=workspace))
+
+
+def _workspace(given, nbytes, dev):
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous() or given.numel() < nbytes:
+        raise ValueError(f"workspace: want at least {nbytes} contiguous uint8 on {dev}, got {given.dtype} "
+                         f"{tuple(given.shape)} on {given.device}")
+    return given
+
+
+def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace):
+    shape, dt, dev = x.shape, x.dtype, x.device
+    code = _dtype_code(dt)
+    if len(shape) != 3:
+        raise ValueError(f"x: want [B, L, D], got {tuple(shape)}")
+    B, L, D = shape
+    _want("x", x, shape, dt, dev)
+    _want("gate", gate, shape, dt, dev)
+    _want("dy", dy, shape, dt, dev)
+    _want("states", states, (int(lib().sscan_glr_states_bytes(B, L, D)) // 4,), torch.float32, dev)
+    if input_gate is not None:
+        _want("input_gate", input_gate, shape, dt, dev)
+    if dh_final is not None:
+        _want("dh_final", dh_final, (B, D), torch.float32, dev)
+    dx, dgate = torch.empty_like(x), torch.empty_like(x)
+    dig = torch.empty_like(x) if input_gate is not None else None
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) if want_dh0 else None
+    drate = None
+    if rate is not None:
+        _want("rate", rate, (D,), torch.float32, dev)
+        drate = torch.empty_like(rate)
+        workspace = _workspace(workspace, int(lib().sscan_glr_backward_workspace_bytes(B, L, D)), dev)
+    else:
+        workspace = None
+    rc = lib().sscan_glr_backward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate),
+                                  states.data_ptr(), dy.data_ptr(), _adr(dh_final), dx.data_ptr(), dgate.data_ptr(),
+                                  _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
+    if rc != OK:
+        raise SscanError(rc, "sscan_glr_backward")
+    return {"dx": dx, "dgate": dgate, "dinput_gate": dig, "drate": drate, "dh0": dh0}
+
+
+def _norm_types(x_dt, r_dt):
+    """(dtype code, residual flag) of a norm whose x and residual have these dtypes."""
+    code = _dtype_code(x_dt)
+    if r_dt == x_dt:
+        return code, 0
+    if r_dt == torch.float32:
+        return code, NORM_RESIDUAL_F32
+    raise TypeError(f"residual of {r_dt} with x of {x_dt} (the same, or float32)")
+
+
+def norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5, rms: bool = False,
+                 want_stats: bool = True, stream=None):
+    """Layer norm over the last axis (``sscan_norm_forward``) on CUDA tensors, after the
+    residual addition when ``residual`` is given.
+
+    x: [..., D] float32 or bfloat16; residual: the shape of x, its dtype or float32;
+    weight, bias: [D] float32 or None; ``rms`` removes no mean.  Returns (y, s, mean, rstd):
+    y in x's dtype; s = x + residual in the residual's dtype (x itself without a residual);
+    mean and rstd float32, one per row (mean None with rms, both None unless
+    ``want_stats``).  Work and new tensors are on ``stream`` (default: the current stream
+    of x's device)."""
+    return _on_device(_norm_forward, x, stream, dict(x=x, weight=weight, bias=bias, residual=residual, eps=eps, rms=rms,
+                                                     want_stats=want_stats))
+
+
+def _norm_forward(st, x, weight, bias, residual, eps, rms, want_stats):
+    shape, dt, dev = x.shape, x.dtype, x.device
+    if len(shape) < 1:
+        raise ValueError("x: want [..., D]")
+    D = shape[-1]
+    code, flags = _norm_types(dt, dt if residual is None else residual.dtype)
+    _want("x", x, shape, dt, dev)
+    s = x
+    if residual is not None:
+        _want("residual", residual, shape, residual.dtype, dev)
+        s = torch.empty_like(residual)
+    if weight is not None:
+        _want("weight", weight, (D,), torch.float32, dev)
+    if bias is not None:
+        _want("bias", bias, (D,), torch.float32, dev)
+    rows = shape[:-1].numel()
+    y = torch.empty_like(x)
+    mean = rstd = None
+    if want_stats:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        mean = None if rms else torch.empty_like(rstd)
+    rc = lib().sscan_norm_forward(rows, D, code, flags | (NORM_RMS if rms else 0), eps, x.data_ptr(), _adr(residual),
+                                  _adr(weight), _adr(bias), y.data_ptr(), None if residual is None else s.data_ptr(),
+                                  _adr(mean), _adr(rstd), st)
+    if rc != OK:
+        raise SscanError(rc, "sscan_norm_forward")
+    return y, s, mean, rstd
+
+
+def norm_backward(dy, s, mean, rstd, weight=None, dresidual=None, rms: bool = False, want_dweight: bool = True,
+                  want_dbias: bool = False, workspace=None, stream=None) -> dict:
+    """Gradients of ``norm_forward`` (``sscan_norm_backward``): dy [..., D] in the forward's
+    dtype of x; s, mean, rstd as it returned them; weight as passed to it; dresidual the
+    gradient that reaches s from its other uses (dtype of s) or None.  Returns a dict with
+    dx (dtype of dy), dresidual (dtype of s; the same tensor as dx where the types are
+    equal), dweight and dbias ([D] float32 or None).  ``workspace``: a CUDA uint8 tensor of
+    at least ``sscan_norm_backward_workspace_bytes`` (default: allocated here)."""
+    return _on_device(_norm_backward, dy, stream, dict(
+        dy=dy, s=s, mean=mean, rstd=rstd, weight=weight, dresidual=dresidual, rms=rms, want_dweight=want_dweight,
+        want_dbias=want_dbias, workspace=workspace))
+
+
+def _norm_backward(st, dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace):
+    shape, dt, dev = dy.shape, dy.dtype, dy.device
+    if len(shape) < 1:
+        raise ValueError("dy: want [..., D]")
+    D = shape[-1]
+    code, flags = _norm_types(dt, s.dtype)
+    _want("dy", dy, shape, dt, dev)
+    _want("s", s, shape, s.dtype, dev)
+    _want("rstd", rstd, shape[:-1], torch.float32, dev)
+    if not rms:
+        if mean is None:
+            raise ValueError("mean: wanted without rms")
+        _want("mean", mean, shape[:-1], torch.float32, dev)
+    elif mean is not None:
+        raise ValueError("mean: must be None with rms")
+    if weight is not None:
+        _want("weight", weight, (D,), torch.float32, dev)
+    if dresidual is not None:
+        _want("dresidual", dresidual, shape, s.dtype, dev)
+    rows = shape[:-1].numel()
+    ds = torch.empty_like(s)
+    dx = torch.empty_like(dy) if s.dtype != dt else None
+    dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
+    dbias = torch.empty((D,), dtype=torch.float32, device=dev) if want_dbias else None
+    if dweight is not None or dbias is not None:
+        workspace = _workspace(workspace, int(lib().sscan_norm_backward_workspace_bytes(rows, D)), dev)
+    else:
+        workspace = None
+    rc = lib().sscan_norm_backward(rows, D, code, flags | (NORM_RMS if rms else 0), dy.data_ptr(), s.data_ptr(),
+                                   _adr(mean), rstd.data_ptr(), _adr(weight), _adr(dresidual), ds.data_ptr(), _adr(dx),
+                                   _adr(dweight), _adr(dbias), _adr(workspace), st)
+    if rc != OK:
+        raise SscanError(rc, "sscan_norm_backward")
+    return {"dx": ds if dx is None else dx, "dresidual": ds, "dweight": dweight, "dbias": dbias}

@@ -4,10 +4,13 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdio>
+#include <cstdlib>
 
 #include "abi_checks.cuh"
 #include "column_sums.cuh"
 #include "kernel_glr.cuh"
+#include "kernel_glr_scan.cuh"
 #include "sscan.h"
 
 using namespace sscan;
@@ -19,29 +22,101 @@ int check_sizes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (B < 1 || D < 1 || L < 0) return SSCAN_ERR_INVALID;
     if (dtype != SSCAN_F32 && dtype != SSCAN_BF16) return SSCAN_ERR_INVALID;
     const int64_t kMax = int64_t(1) << 31;
-    if (B >= kMax || D >= kMax || B * D >= kMax * 16) return SSCAN_ERR_UNSUPPORTED;
+    if (B >= kMax || D >= kMax || B * D >= kMax) return SSCAN_ERR_UNSUPPORTED;
     if (L > (int64_t(1) << 40) || (L > 0 && B * D > (int64_t(1) << 48) / L)) return SSCAN_ERR_UNSUPPORTED;
     return SSCAN_OK;
 }
 
 int64_t runs(int64_t L) { return ceil_div(L, glr::kRun); }
 
+// How a scan is spread: warps of a block and blocks of a cluster along the sequence, or
+// (warps = 0) one thread per channel.
+struct Shape {
+    int warps, cluster;
+};
+
+Shape scan_shape(int64_t B, int64_t L, int64_t D, int ch) {
+#ifdef GLR_TUNE
+    if (const char *e = getenv("GLR_TUNE")) { Shape s; int w, c; if (sscanf(e, "%d,%d", &w, &c) == 2) return Shape{w, c}; }
+#endif
+    if (L <= 4) return {0, 1};
+    const int64_t n = runs(L), chains = B * ceil_div(D, ch);
+    int w = 1, c = 1;
+    while (w < glr::kMaxWarps && w < n) w *= 2;
+    while (c < glr::kMaxCluster && c * w < n && chains * c * w < 148 * 16) c *= 2;
+    return {w, c};
+}
+
+template <class IO>
+bool staged(int64_t D) { return D * int64_t(sizeof(IO)) % 16 == 0; }
+
+// Blocks, cluster and shared memory of a scan kernel's launch, on stream s.
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    Launch(int64_t blocks, const Shape &sh, int smem, cudaStream_t s) {
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+        cfg.blockDim = dim3(32 * sh.warps);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = sh.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
+    }
+};
+
+template <class IO, bool STAGED, bool DECAY, bool IG>
+int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
+    constexpr int NS = IG ? 3 : 2, ch = 32 * glr::lane_channels<IO, STAGED>();
+    const Shape sh = scan_shape(p.B, p.L, p.D, ch);
+    if (sh.warps == 0) {
+        constexpr int V = STAGED ? 2 : 1;
+        const int64_t blocks = ceil_div(p.B * p.D, V * glr::kStepThreads);
+        glr::glr_step_kernel<IO, V, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
+    }
+#ifdef GLR_K
+    constexpr int K = GLR_K;
+#else
+    constexpr int K = glr::kRun;
+#endif
+    constexpr auto kern = glr::glr_scan_kernel<IO, STAGED, DECAY, IG, K>;
+    if (smem_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
+        return SSCAN_ERR_CUDA;
+    const int64_t groups = ceil_div(p.D, ch), blocks = p.B * groups * sh.cluster;
+    Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, K>(sh.warps, sh.cluster), s);
+    return cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) == cudaSuccess ? SSCAN_OK
+                                                                                                       : SSCAN_ERR_CUDA;
+}
+
 template <class IO, bool DECAY, bool IG>
 int launch_forward(const glr::FwdParams &p, cudaStream_t s) {
-    const int64_t blocks = ceil_div(p.B * p.D, glr::kStepThreads);
-    glr::glr_step_kernel<IO, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
+    return staged<IO>(p.D) ? launch_scan<IO, true, DECAY, IG>(p, s) : launch_scan<IO, false, DECAY, IG>(p, s);
+}
+
+template <class IO, bool STAGED, bool DECAY, bool IG>
+int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
+    constexpr int NS = IG ? 4 : 3, ch = 32 * glr::lane_channels<IO, STAGED>();
+    Shape sh = scan_shape(p.B, p.L, p.D, ch);
+    if (sh.warps == 0) sh.warps = 1;
+    constexpr auto kern = glr::glr_scan_backward_kernel<IO, STAGED, DECAY, IG>;
+    if (smem_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
+        return SSCAN_ERR_CUDA;
+    const int64_t groups = ceil_div(p.D, ch), blocks = p.B * groups * sh.cluster;
+    Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(sh.warps, sh.cluster), s);
+    if (cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) != cudaSuccess) return SSCAN_ERR_CUDA;
+    if (!DECAY) return SSCAN_OK;
+    const ColumnSums cs = {p.part, {drate, nullptr}, p.B * sh.cluster, p.D, 0};
+    column_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(p.D, 32))), kColThreads, 0, s>>>(cs);
     return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
 }
 
 template <class IO, bool DECAY, bool IG>
 int launch_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
-    const int64_t blocks = ceil_div(p.B * p.D, glr::kStepThreads);
-    glr::glr_step_backward_kernel<IO, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SSCAN_ERR_CUDA;
-    if (!DECAY) return SSCAN_OK;
-    const ColumnSums cs = {p.part, {drate, nullptr}, p.B, p.D, 0};
-    column_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(p.D, 32))), kColThreads, 0, s>>>(cs);
-    return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
+    return staged<IO>(p.D) ? launch_scan_backward<IO, true, DECAY, IG>(p, drate, s)
+                           : launch_scan_backward<IO, false, DECAY, IG>(p, drate, s);
 }
 
 template <class IO>
@@ -97,7 +172,7 @@ int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x,
 
 size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
     if (check_sizes(B, L, D, SSCAN_F32) != SSCAN_OK || L == 0) return 0;
-    return round_up_256(size_t(B) * size_t(D) * sizeof(float));
+    return round_up_256(size_t(B) * glr::kMaxCluster * size_t(D) * sizeof(float));
 }
 
 int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,

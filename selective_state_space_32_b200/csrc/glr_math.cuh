@@ -1,15 +1,18 @@
-// glr_math.cuh -- the gate arithmetic of the gated linear recurrence, one token of one
-// channel, in fp32.
+// glr_math.cuh -- the gate arithmetic of the gated linear recurrence in fp32, two values
+// at a time (two channels of a token, or two tokens of a channel) as packed pairs: the
+// kernels are near their issue rate, and a packed operation takes one slot for two values.
 //
-// s = sigmoid(g) and its complement n = 1 - s come from t = e^-|g| <= 1: one of them is
-// 1/(1 + t), the other t/(1 + t), so neither cancels nor overflows (g = +-inf gives 1
-// and 0).  Without a rate the decay is a = s and the input factor beta = n.  With a
-// rate c, a = e^-z, z = c s, and beta = sqrt(1 - a^2) = sqrt(m (2 - m)) with
-// m = 1 - a.  m cancels when z is small, where a long memory lives, so there
-// (z <= 1/8) m = z phi(-z), phi(z) = (e^z - 1)/z by the polynomial psi2 (3.3e-7
-// relative), and a = 1 - m (correctly rounded up to that: the error of a slow decay
-// is not the MUFU's 2^-22 times the horizon 1/(1 - a)); beyond, a = 2^(-z log2 e) on
-// the MUFU and m = 1 - a >= 0.117.
+// sigmoid(g) = 1 / (1 + E), E = e^-g: accurate relative to its size for every g, since
+// nothing cancels (E overflowing gives 0).  Its complement is E sigmoid(g), with E's
+// exponent held below 126 so that the product stays finite.
+//
+// A rate c gives the decay a = e^-z, z = c s, and beta = sqrt(1 - a^2) = sqrt(m (2 - m))
+// with m = 1 - a.  m must keep its digits when z is small, where a long memory lives, so
+// both come from one range reduction: e = z log2 e = j + f with j = round(e),
+// p = 2^-f - 1 = f times a polynomial (no constant term: relative accuracy at f -> 0),
+// S = 2^-j, a = S + S p and m = (1 - S) - S p, which is -p itself when j = 0.  It runs on
+// the FMA pipe: the MUFU has 16 lanes an SM and clock, and with the sigmoids and the
+// square root the exponential would make it the bound.
 #pragma once
 
 #include "device_utils.cuh"
@@ -18,15 +21,11 @@ namespace sscan {
 namespace glr {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 __device__ __forceinline__ float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float sqrt_approx(float x) {
-    float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float rsqrt_approx(float x) {
@@ -34,26 +33,115 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-// s = sigmoid(g), n = 1 - s
-__device__ __forceinline__ void sigmoid_pair(float g, float &s, float &n) {
-    const float t = ex2(-fabsf(g) * kLog2e);
-    const float big = rcp(1.0f + t), small = t * big;
-    s = g >= 0.0f ? big : small;
-    n = g >= 0.0f ? small : big;
+// min that keeps NaN
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+template <class F>
+__device__ __forceinline__ f2 map2(f2 v, F f) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(f(a), f(b));
 }
 
-// a = e^-z and m = 1 - a for z = c s >= 0 (c in nats)
-__device__ __forceinline__ void decay(float z, float &a, float &m) {
-    const float e = z * kLog2e;
-    float q = fmaf(-1.387602649629116e-02f, e, 8.013805747032166e-02f);  // psi2 at -e, scalar
-    q = fmaf(q, -e, 3.4657374024391174e-01f);
-    q = fmaf(q, -e, 9.999997615814209e-01f);
-    const float ms = z * q;
-    const float al = ex2(-e);
-    const bool slow = z <= 0.125f;
-    m = slow ? ms : 1.0f - al;
-    a = slow ? 1.0f - ms : al;
+// 1 + e^-g
+__device__ __forceinline__ f2 one_plus_exp(f2 g) {
+    return add2(map2(mul2(g, splat2(-kLog2e)), [](float e) { return ex2(e); }), splat2(1.0f));
+}
+__device__ __forceinline__ f2 rcp2(f2 v) {
+    return map2(v, [](float x) { return rcp(x); });
+}
+// s = sigmoid(g), n = 1 - s
+__device__ __forceinline__ void sigmoid2(f2 g, f2 &s, f2 &n) {
+    const f2 E = map2(mul2(g, splat2(-kLog2e)), [](float e) { return ex2(min_nan(e, 126.0f)); });
+    s = rcp2(add2(E, splat2(1.0f)));
+    n = mul2(E, s);
+}
+
+// a = e^-z and m = 1 - a, z = s c, from s >= 0 and cl = c log2 e >= 0.
+// 2^-f - 1 = (-f) q(-f) with q = ln 2 times the degree-5 minimax polynomial of (e^z - 1)/z on
+// |f| <= 1/2 (csrc/gen_phi_poly.py 5 0.3465735902799726 --log2: 1.1e-8, 1.4e-7 evaluated in fp32).
+__device__ __forceinline__ void decay2(f2 s, f2 cl, f2 &a, f2 &m) {
+    const f2 kShift = splat2(12582912.0f);  // 1.5 * 2^23
+    const f2 e = map2(mul2(s, cl), [](float v) { return min_nan(v, 125.0f); });
+    const f2 t = add2(e, kShift);           // j in the low mantissa bits
+    const f2 f = fma2(e, splat2(-1.0f), add2(t, splat2(-12582912.0f)));  // j - e = -f, exact
+    f2 q = fma2(splat2(1.5403512225020677e-04f), f, splat2(1.3390735257416964e-03f));
+    q = fma2(q, f, splat2(9.6182376146316528e-03f));
+    q = fma2(q, f, splat2(5.5503576993942261e-02f));
+    q = fma2(q, f, splat2(2.4022650718688965e-01f));
+    q = fma2(q, f, splat2(6.9314718246459961e-01f));
+    const f2 p = mul2(q, f);
+    float t0, t1;
+    unpack2(t, t0, t1);
+    const f2 S = pack2(__uint_as_float(0x3f800000u - (__float_as_uint(t0) << 23)),
+                       __uint_as_float(0x3f800000u - (__float_as_uint(t1) << 23)));
+    const f2 Sp = mul2(S, p);
+    a = add2(S, Sp);
+    m = add2(add2(splat2(1.0f), neg2(S)), neg2(Sp));
+}
+
+// Two tokens' or channels' decay a and input b = beta sigmoid(ig) x.  cl: rate log2 e.
+template <bool DECAY, bool IG>
+__device__ __forceinline__ void token2(f2 x, f2 g, f2 ig, f2 cl, f2 &a, f2 &b) {
+    if constexpr (DECAY) {
+        f2 m;
+        decay2(rcp2(one_plus_exp(g)), cl, a, m);
+        const f2 w = mul2(m, add2(splat2(2.0f), neg2(m)));
+        f2 v = add2(w, splat2(kTiny));  // w = 0 (a = 1) gives beta = 0, not 0 * inf
+        // beta sigmoid(ig) = sqrt(w) / (1 + E) = w rsqrt(w (1 + E)^2): one MUFU operation
+        // for the square root and the quotient
+        if constexpr (IG) {
+            const f2 q = one_plus_exp(ig);
+            v = mul2(v, mul2(q, q));
+        }
+        b = mul2(mul2(w, map2(v, [](float y) { return rsqrt_approx(y); })), x);
+    } else {
+        f2 n;
+        sigmoid2(g, a, n);
+        if constexpr (IG) x = mul2(x, rcp2(one_plus_exp(ig)));
+        b = mul2(n, x);
+    }
+}
+
+// Two tokens' or channels' factors of the gradients that need no state: with G the whole
+// gradient of h_t,  dx = G px,  dig = G pi,  dgate = G kg (h_{t-1} - v),
+// drate += G kr (h_{t-1} - v):
+//   dh/da = h_{t-1} + u dbeta/da;  no rate: dbeta/da = -1, da/dg = s n: v = u, kg = s n
+//   rate: dbeta/da = -a/beta, da/dz = -a, dz/dc = s, dz/dg = c s n: v = a u / beta,
+//   kr = -s a, kg = kr c n.
+// a/beta diverges as z -> 0, but s a^2/beta -> 0 with it: 1/beta is taken of at least
+// 2^-126, which keeps every product finite and its limit 0.
+template <bool DECAY, bool IG>
+__device__ __forceinline__ void token_grad2(f2 x, f2 g, f2 ig, f2 c, f2 cl, f2 &a, f2 &b, f2 &v, f2 &px, f2 &pi, f2 &kg,
+                                            f2 &kr) {
+    f2 s, n, si = 0, ni = 0, u = x, beta;
+    sigmoid2(g, s, n);
+    if constexpr (IG) {
+        sigmoid2(ig, si, ni);
+        u = mul2(x, si);
+    }
+    if constexpr (DECAY) {
+        f2 m;
+        decay2(s, cl, a, m);
+        const f2 w = mul2(m, add2(splat2(2.0f), neg2(m)));
+        const f2 ib = map2(add2(w, splat2(kTiny)), [](float y) { return rsqrt_approx(y); });
+        beta = mul2(w, ib);
+        v = mul2(mul2(a, ib), u);
+        kr = neg2(mul2(s, a));
+        kg = mul2(kr, mul2(c, n));
+    } else {
+        a = s;
+        beta = n;
+        v = u;
+        kr = 0;
+        kg = mul2(s, n);
+    }
+    b = mul2(beta, u);
+    px = IG ? mul2(beta, si) : beta;
+    pi = IG ? mul2(b, ni) : 0;
 }
 
 }  // namespace glr

@@ -1,0 +1,445 @@
+// kernel_glr_scan.cuh -- the gated linear recurrence over a sequence, parallel along it.
+//
+// A token is the affine map h -> a h + b, and maps compose: (a2, b2) after (a1, b1) is
+// (a1 a2, a2 b1 + b2).  A warp owns a run of K tokens of kRowBytes = 128 bytes of
+// channels (64 in bf16, two a lane; 32 in fp32), a block W consecutive runs, a cluster
+// of C blocks C W consecutive runs, and the cluster walks the sequence of one batch row
+// and channel group in steps of C W runs:
+//   1. every warp computes a and b of its run (registers) and the run's composition;
+//   2. the block's warps exchange compositions through shared memory, and the cluster's
+//      blocks the blocks' through distributed shared memory (one cluster barrier);
+//   3. every thread applies what precedes its run to the carried state, walks its
+//      tokens once more and stores them; the carried state moves on by the composition
+//      of the whole step, which every block forms for itself in the same order.
+// So x and the gates are read once, y is written once, nothing goes through a workspace,
+// no block waits on a flag, and the order of the sums depends on the sizes only.  The
+// next steps' inputs arrive by cp.async in a ring of each warp's own while this one runs.
+// The backward pass is the same walk from the last token: G_t = dy_t + e, e <- a_t G_t is
+// a map of e, with the states of a run recomputed from the saved state before it.
+//
+// Rows that are not a multiple of 16 bytes cannot be copied by cp.async 16 bytes at a
+// time; STAGED = false loads them from memory, one channel a lane.
+#pragma once
+
+#include "device_utils.cuh"
+#include "glr_math.cuh"
+#include "kernel_glr.cuh"
+
+namespace sscan {
+namespace glr {
+
+constexpr int kRowBytes = 128;
+constexpr int kMaxWarps = 8;
+constexpr int kMaxCluster = 8;
+constexpr int kStages = 2;
+
+// channels a lane holds
+template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
+
+template <class IO, bool STAGED, int NS, int K>
+constexpr int scan_smem_bytes(int warps, int cluster) {
+    const int ch = 32 * lane_channels<IO, STAGED>();
+    return (STAGED ? warps * kStages * NS * K * kRowBytes : 0) + 2 * (warps + cluster) * ch * 8;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A lane's V channels: one value, or a packed pair.
+template <int V> struct Lane;
+template <> struct Lane<1> {
+    using T = float;
+    static __device__ __forceinline__ float mul(float a, float b) { return a * b; }
+    static __device__ __forceinline__ float add(float a, float b) { return a + b; }
+    static __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+    static __device__ __forceinline__ float splat(float v) { return v; }
+    static __device__ __forceinline__ float load(const float *p) { return *p; }
+    static __device__ __forceinline__ void store(float *p, float v) { *p = v; }
+    // token k of an array of pairs: half k % 2 of pair k / 2
+    template <int NP> static __device__ __forceinline__ float get(const f2 (&v)[NP], int k) {
+        float a, b;
+        unpack2(v[k / 2], a, b);
+        return k & 1 ? b : a;
+    }
+    template <int NP> static __device__ __forceinline__ void set(f2 (&v)[NP], int k, float x) {
+        float a, b;
+        unpack2(v[k / 2], a, b);
+        v[k / 2] = k & 1 ? pack2(a, x) : pack2(x, b);
+    }
+};
+template <> struct Lane<2> {
+    using T = f2;
+    static __device__ __forceinline__ f2 mul(f2 a, f2 b) { return mul2(a, b); }
+    static __device__ __forceinline__ f2 add(f2 a, f2 b) { return add2(a, b); }
+    static __device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+    static __device__ __forceinline__ f2 splat(float v) { return splat2(v); }
+    static __device__ __forceinline__ f2 load(const float *p) { return pack2(p[0], p[1]); }
+    static __device__ __forceinline__ void store(float *p, f2 v) { store_channels<float, 2>(p, v); }
+    // token k of an array of pairs: pair k
+    template <int NP> static __device__ __forceinline__ f2 get(const f2 (&v)[NP], int k) { return v[k]; }
+    template <int NP> static __device__ __forceinline__ void set(f2 (&v)[NP], int k, f2 x) { v[k] = x; }
+};
+template <class IO> __device__ __forceinline__ void store_lane(IO *p, float v) { Io<IO>::st(p, v); }
+template <class IO> __device__ __forceinline__ void store_lane(IO *p, f2 v) { store_channels<IO, 2>(p, v); }
+
+// One warp's view of its streams: NS tensors [B][L][D] in runs of K tokens, and a lane's
+// V channels of them as pairs (V = 2: the channels of one token; V = 1: two tokens).
+template <class IO, bool STAGED, int NS, int K>
+struct RunLoader {
+    static constexpr int V = lane_channels<IO, STAGED>();
+    static constexpr int CH = 32 * V, NP = K * V / 2;
+    static constexpr int kStageBytes = NS * K * kRowBytes;
+    const IO *src[NS];  // batch row's first token, first channel of the group
+    unsigned char *ring;
+    int64_t L, D;
+    int lane, live;  // live: channels of the group that exist
+
+    // Start copying the run of tokens t0 .. t0 + K - 1 (tokens past L, channels past D: zeros).
+    __device__ __forceinline__ void issue(int64_t t0, int stage) const {
+        if constexpr (STAGED) {
+            if (t0 >= 0 && t0 < L) {
+                const int col = (lane & 7) * (16 / Io<IO>::kBytes), row = lane >> 3;
+                const int n = col < live ? (L - t0 < K ? static_cast<int>(L - t0) : K) : 0;
+                const int64_t at = t0 * D + row * D + col;
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int h = 0; h < K / 4; ++h)
+                        cp_async16(ring + stage * kStageBytes + (s * K + row + 4 * h) * kRowBytes + (lane & 7) * 16,
+                                   row + 4 * h < n ? src[s] + at + 4 * h * D : src[s], row + 4 * h < n);
+            }
+            cp_async_commit();
+        }
+    }
+    // stream s, pair i of the run at t0 with n tokens
+    __device__ __forceinline__ f2 pair(int64_t t0, int n, int stage, int s, int i) const {
+        if constexpr (STAGED) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(ring + stage * kStageBytes + s * K * kRowBytes) + lane;
+            if constexpr (V == 2) {
+                const uint32_t v = w[i * 32];
+                return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+            } else {
+                return pack2(__uint_as_float(w[2 * i * 32]), __uint_as_float(w[(2 * i + 1) * 32]));
+            }
+        } else {
+            const IO *p = src[s] + (t0 + 2 * i) * D + lane;
+            const bool on = lane < live;
+            return pack2(on && 2 * i < n ? Io<IO>::widen(Io<IO>::ld(p)) : 0.0f,
+                         on && 2 * i + 1 < n ? Io<IO>::widen(Io<IO>::ld(p + D)) : 0.0f);
+        }
+    }
+};
+
+// (decay, offset) of one lane's channels in shared memory: V * 8 bytes
+__device__ __forceinline__ void load_map(const float2 *p, float &a, float &h) {
+    const float2 m = *p;
+    a = m.x, h = m.y;
+}
+__device__ __forceinline__ void load_map(const float2 *p, f2 &a, f2 &h) {
+    const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(p);
+    a = m.x, h = m.y;
+}
+__device__ __forceinline__ void store_map(float2 *p, float a, float h) { *p = make_float2(a, h); }
+__device__ __forceinline__ void store_map(float2 *p, f2 a, f2 h) {
+    *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(a, h);
+}
+// The same at the address that `local` (shared memory of this block) has in block `rank`.
+__device__ __forceinline__ uint32_t cluster_address(const void *local, uint32_t rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ void send_map(float2 *local, uint32_t rank, float a, float h) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_address(local, rank)), "f"(a), "f"(h) : "memory");
+}
+__device__ __forceinline__ void send_map(float2 *local, uint32_t rank, f2 a, f2 h) {
+    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(cluster_address(local, rank)), "l"(a), "l"(h) : "memory");
+}
+
+// The exchange of one step.  In: the composition (A, H) of this warp's run, the state
+// `carry` before the step.  Returns the state before the run; `carry` becomes the state
+// after the step.  agg: [2][warps][CH], cl: [2][C][CH] maps; `par` alternates, so that a
+// step's entries are overwritten only after a barrier that follows their last reading.
+template <int V>
+__device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, typename Lane<V>::T H,
+                                                        typename Lane<V>::T &carry, float2 *agg, float2 *cl, int par,
+                                                        int warps, int w, uint32_t C, uint32_t rank, int lane) {
+    using LV = Lane<V>;
+    using T = typename LV::T;
+    constexpr int CH = 32 * V;
+    const float2 *at = agg + par * warps * CH + lane * V;
+    __syncwarp();
+    if (warps > 1) {
+        store_map(agg + (par * warps + w) * CH + lane * V, A, H);
+        __syncthreads();
+    }
+    if (C == 1) {
+        if (warps == 1) {
+            const T h = carry;
+            carry = LV::fma(A, carry, H);
+            return h;
+        }
+        T h = carry;
+        for (int q = 0; q < warps; ++q, at += CH) {
+            T ma, mh;
+            load_map(at, ma, mh);
+            if (q == w) h = carry;
+            carry = LV::fma(ma, carry, mh);
+        }
+        return h;
+    }
+    // the runs of this block before this one; the warps that send go on to the whole block
+    T Ab = LV::splat(1.0f), Hb = LV::splat(0.0f);
+    int q = 0;
+    for (; q < w; ++q, at += CH) {
+        T ma, mh;
+        load_map(at, ma, mh);
+        Ab = LV::mul(ma, Ab);
+        Hb = LV::fma(ma, Hb, mh);
+    }
+    const T Ap = Ab, Hp = Hb;
+    if (static_cast<uint32_t>(w) < C) {
+        if (warps == 1) {
+            Ab = A, Hb = H;
+        } else {
+            for (; q < warps; ++q, at += CH) {
+                T ma, mh;
+                load_map(at, ma, mh);
+                Ab = LV::mul(ma, Ab);
+                Hb = LV::fma(ma, Hb, mh);
+            }
+        }
+        for (uint32_t r = w; r < C; r += warps) send_map(cl + (par * C + rank) * CH + lane * V, r, Ab, Hb);
+        __syncwarp();
+    }
+    cluster_arrive();
+    cluster_wait();
+    at = cl + par * C * CH + lane * V;
+    T h = carry;
+    for (uint32_t r = 0; r < C; ++r, at += CH) {
+        T ma, mh;
+        load_map(at, ma, mh);
+        if (r == rank) h = carry;
+        carry = LV::fma(ma, carry, mh);
+    }
+    return LV::fma(Ap, h, Hp);
+}
+
+// grid: B * groups * C blocks of 32 W threads in clusters of C
+template <class IO, bool STAGED, bool DECAY, bool IG, int K>
+__global__ void __launch_bounds__(32 * kMaxWarps, K == 8 ? 3 : 2) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
+    constexpr int NS = IG ? 3 : 2;
+    using Loader = RunLoader<IO, STAGED, NS, K>;
+    constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
+    using LV = Lane<V>;
+    using T = typename LV::T;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t rank = C > 1 ? cluster_rank() : 0;
+    if (C > 1) cluster_arrive();
+    const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
+    const int64_t row0 = b * p.L * p.D + ch0;
+    Loader in;
+    in.src[0] = static_cast<const IO *>(p.x) + row0;
+    in.src[1] = static_cast<const IO *>(p.gate) + row0;
+    if constexpr (IG) in.src[2] = static_cast<const IO *>(p.igate) + row0;
+    in.ring = smem + w * kStages * Loader::kStageBytes;
+    in.L = p.L, in.D = p.D, in.lane = lane;
+    in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
+    const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
+    int64_t t0 = (static_cast<int64_t>(rank) * warps + w) * K;
+    const int64_t steps = (p.L + step - 1) / step;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) in.issue(t0 + s * step, s);
+    float2 *agg = reinterpret_cast<float2 *>(smem + (STAGED ? warps * kStages * Loader::kStageBytes : 0));
+    float2 *cl = agg + 2 * warps * CH;
+    const bool mine = lane * V < in.live;
+    T carry = LV::splat(0.0f);
+    f2 cc = 0;  // rate log2 e of the pair
+    if (mine) {
+        if constexpr (DECAY) {
+            if constexpr (V == 2) cc = mul2(LV::load(p.rate + ch0 + lane * V), splat2(kLog2e));
+            else cc = splat2(p.rate[ch0 + lane] * kLog2e);
+        }
+        if (p.h0) carry = LV::load(p.h0 + b * p.D + ch0 + lane * V);
+    }
+    IO *y = static_cast<IO *>(p.y) + row0 + lane * V;
+    float *states = p.states ? p.states + b * p.nruns * p.D + ch0 + lane * V : nullptr;
+    __syncwarp();
+    if (C > 1) cluster_wait();  // every block of the cluster has started: its shared memory may be written
+    int stage = 0;
+    for (int64_t it = 0; it < steps; ++it, t0 += step) {
+        const int n = t0 >= p.L ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
+        f2 a[NP], bb[NP];
+        if constexpr (STAGED) {
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+        }
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                token2<DECAY, IG>(in.pair(t0, n, stage, 0, i), in.pair(t0, n, stage, 1, i),
+                                  IG ? in.pair(t0, n, stage, NS - 1, i) : 0, cc, a[i], bb[i]);
+        }
+        if (n < K) {  // tokens past the end: the identity
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k >= n) LV::set(a, k, LV::splat(1.0f)), LV::set(bb, k, LV::splat(0.0f));
+        }
+        T A = LV::get(a, 0), H = LV::get(bb, 0);
+#pragma unroll
+        for (int k = 1; k < K; ++k) {
+            A = LV::mul(A, LV::get(a, k));
+            H = LV::fma(LV::get(a, k), H, LV::get(bb, k));
+        }
+        __syncwarp();
+        in.issue(t0 + kStages * step, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        T h = exchange<V>(A, H, carry, agg, cl, static_cast<int>(it & 1), warps, w, C, rank, lane);
+        if (mine) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (k >= n) break;
+                if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D, h);
+                h = LV::fma(LV::get(a, k), h, LV::get(bb, k));
+                store_lane<IO>(y + (t0 + k) * p.D, h);
+            }
+        }
+    }
+    if (p.h_final && rank == 0 && w == 0 && mine) LV::store(p.h_final + b * p.D + ch0 + lane * V, carry);
+}
+
+// The walk from the last token.  part (with a rate): row b * C + rank holds the sums of
+// this block's channels.
+template <class IO, bool STAGED, bool DECAY, bool IG>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
+    constexpr int NS = IG ? 4 : 3, K = kRun;
+    using Loader = RunLoader<IO, STAGED, NS, K>;
+    constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
+    using LV = Lane<V>;
+    using T = typename LV::T;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t rank = C > 1 ? cluster_rank() : 0;
+    if (C > 1) cluster_arrive();
+    const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
+    const int64_t row0 = b * p.L * p.D + ch0;
+    Loader in;
+    in.src[0] = static_cast<const IO *>(p.x) + row0;
+    in.src[1] = static_cast<const IO *>(p.gate) + row0;
+    in.src[2] = static_cast<const IO *>(p.dy) + row0;
+    if constexpr (IG) in.src[3] = static_cast<const IO *>(p.igate) + row0;
+    in.ring = smem + w * kStages * Loader::kStageBytes;
+    in.L = p.L, in.D = p.D, in.lane = lane;
+    in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
+    const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
+    int64_t t0 = (p.nruns - 1 - (static_cast<int64_t>(rank) * warps + w)) * K;  // this warp's run of the first step
+    const int64_t steps = (p.nruns * K + step - 1) / step;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) in.issue(t0 - s * step, s);
+    float2 *agg = reinterpret_cast<float2 *>(smem + (STAGED ? warps * kStages * Loader::kStageBytes : 0));
+    float2 *cl = agg + 2 * warps * CH;
+    const bool mine = lane * V < in.live;
+    T carry = LV::splat(0.0f), dc = LV::splat(0.0f);
+    f2 cn = 0, cl2 = 0;  // the pair's rate, and rate log2 e
+    if (mine) {
+        if constexpr (DECAY) {
+            if constexpr (V == 2) cn = LV::load(p.rate + ch0 + lane * V);
+            else cn = splat2(p.rate[ch0 + lane]);
+            cl2 = mul2(cn, splat2(kLog2e));
+        }
+        if (p.dh_final) carry = LV::load(p.dh_final + b * p.D + ch0 + lane * V);
+    }
+    const int64_t out0 = row0 + lane * V;
+    __syncwarp();
+    if (C > 1) cluster_wait();
+    int stage = 0;
+    for (int64_t it = 0; it < steps; ++it, t0 -= step) {
+        const int n = t0 < 0 ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
+        f2 a[NP], g[NP], px[NP], pi[NP], pg[NP], pr[NP];
+        T h = LV::splat(0.0f);
+        if (mine && n > 0) h = LV::load(p.states + (b * p.nruns + t0 / K) * p.D + ch0 + lane * V);
+        if constexpr (STAGED) {
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+        }
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                f2 bb, v, kg, kr, d;
+                g[i] = in.pair(t0, n, stage, 2, i);
+                token_grad2<DECAY, IG>(in.pair(t0, n, stage, 0, i), in.pair(t0, n, stage, 1, i),
+                                       IG ? in.pair(t0, n, stage, NS - 1, i) : 0, cn, cl2, a[i], bb, v, px[i], pi[i], kg, kr);
+                if constexpr (V == 2) {
+                    d = add2(h, neg2(v));
+                    h = fma2(a[i], h, bb);
+                } else {  // two tokens of one channel: the second's state follows from the first's
+                    float a0, a1, b0, b1;
+                    unpack2(a[i], a0, a1);
+                    unpack2(bb, b0, b1);
+                    const float h1 = fmaf(a0, h, b0);
+                    d = add2(pack2(h, h1), neg2(v));
+                    h = fmaf(a1, h1, b1);
+                }
+                pg[i] = mul2(kg, d);
+                pr[i] = mul2(kr, d);
+            }
+        }
+        if (n < K) {  // tokens past the end: the identity (and no part in the rate's sum)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k >= n) {
+                    LV::set(a, k, LV::splat(1.0f));
+                    LV::set(g, k, LV::splat(0.0f));
+                    if constexpr (DECAY) LV::set(pr, k, LV::splat(0.0f));
+                }
+        }
+        T A = LV::splat(1.0f), F = LV::splat(0.0f);
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {  // e -> a (g + e), last token first
+            F = LV::mul(LV::get(a, k), LV::add(LV::get(g, k), F));
+            A = LV::mul(A, LV::get(a, k));
+        }
+        __syncwarp();
+        in.issue(t0 - kStages * step, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        T e = exchange<V>(A, F, carry, agg, cl, static_cast<int>(it & 1), warps, w, C, rank, lane);
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            const T G = LV::add(LV::get(g, k), e);
+            e = LV::mul(LV::get(a, k), G);
+            if constexpr (DECAY) dc = LV::fma(G, LV::get(pr, k), dc);
+            if (mine && k < n) {
+                const int64_t at = out0 + (t0 + k) * p.D;
+                store_lane<IO>(static_cast<IO *>(p.dx) + at, LV::mul(G, LV::get(px, k)));
+                store_lane<IO>(static_cast<IO *>(p.dgate) + at, LV::mul(G, LV::get(pg, k)));
+                if constexpr (IG) store_lane<IO>(static_cast<IO *>(p.digate) + at, LV::mul(G, LV::get(pi, k)));
+            }
+        }
+    }
+    if (p.dh0 && rank == 0 && w == 0 && mine) LV::store(p.dh0 + b * p.D + ch0 + lane * V, carry);
+    if constexpr (DECAY) {
+        float *sums = reinterpret_cast<float *>(agg);  // [warps][CH], once the last step's entries are read
+        __syncthreads();
+        LV::store(sums + w * CH + lane * V, dc);
+        __syncthreads();
+        if (w == 0 && mine) {
+            for (int q = 1; q < warps; ++q) dc = LV::add(dc, LV::load(sums + q * CH + lane * V));
+            LV::store(p.part + (b * C + rank) * p.D + ch0 + lane * V, dc);
+        }
+    }
+}
+
+}  // namespace glr
+}  // namespace sscan

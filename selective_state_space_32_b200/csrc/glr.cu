@@ -77,11 +77,7 @@ int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
         glr::glr_step_kernel<IO, V, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
         return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
     }
-#ifdef GLR_K
-    constexpr int K = GLR_K;
-#else
-    constexpr int K = glr::kRun;
-#endif
+    constexpr int K = glr::kForwardRun;
     constexpr auto kern = glr::glr_scan_kernel<IO, STAGED, DECAY, IG, K>;
     if (smem_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;

@@ -60,27 +60,36 @@ __device__ __forceinline__ void sigmoid2(f2 g, f2 &s, f2 &n) {
     n = mul2(E, s);
 }
 
-// a = e^-z and m = 1 - a, z = s c, from s >= 0 and cl = c log2 e >= 0.
-// 2^-f - 1 = (-f) q(-f) with q = ln 2 times the degree-5 minimax polynomial of (e^z - 1)/z on
-// |f| <= 1/2 (csrc/gen_phi_poly.py 5 0.3465735902799726 --log2: 1.1e-8, 1.4e-7 evaluated in fp32).
+// a - v on the FMA pipe (flipping the sign bits would be two integer operations)
+__device__ __forceinline__ f2 minus2(f2 a, f2 v) { return fma2(v, splat2(-1.0f), a); }
+
+// The rate times log2 e of two channels.  Rates above 80 act as 80 (a decay of 2e-35 at
+// s = 1): z stays in the range of the exponent arithmetic below without a test per token.
+constexpr float kMaxRate = 80.0f;
+__device__ __forceinline__ f2 capped_rate(f2 c) {
+    return map2(c, [](float v) { return min_nan(v, kMaxRate); });
+}
+
+// a = e^-z and m = 1 - a, z = s c, from s in [0, 1] and cl = c log2 e.
+// 2^-f - 1 = f q(f), with -q(-f) = ln 2 times the degree-5 minimax polynomial of (e^z - 1)/z
+// on |f| <= 1/2 (csrc/gen_phi_poly.py 5 0.3465735902799726 --log2: 1.1e-8, 1.4e-7 evaluated
+// in fp32).
 __device__ __forceinline__ void decay2(f2 s, f2 cl, f2 &a, f2 &m) {
     const f2 kShift = splat2(12582912.0f);  // 1.5 * 2^23
-    const f2 e = map2(mul2(s, cl), [](float v) { return min_nan(v, 125.0f); });
-    const f2 t = add2(e, kShift);           // j in the low mantissa bits
-    const f2 f = fma2(e, splat2(-1.0f), add2(t, splat2(-12582912.0f)));  // j - e = -f, exact
-    f2 q = fma2(splat2(1.5403512225020677e-04f), f, splat2(1.3390735257416964e-03f));
+    const f2 t = fma2(s, cl, kShift);       // j in the low mantissa bits
+    const f2 f = fma2(s, cl, minus2(kShift, t));  // e - j
+    f2 q = fma2(splat2(1.5403512225020677e-04f), f, splat2(-1.3390735257416964e-03f));
     q = fma2(q, f, splat2(9.6182376146316528e-03f));
-    q = fma2(q, f, splat2(5.5503576993942261e-02f));
+    q = fma2(q, f, splat2(-5.5503576993942261e-02f));
     q = fma2(q, f, splat2(2.4022650718688965e-01f));
-    q = fma2(q, f, splat2(6.9314718246459961e-01f));
+    q = fma2(q, f, splat2(-6.9314718246459961e-01f));
     const f2 p = mul2(q, f);
     float t0, t1;
     unpack2(t, t0, t1);
-    const f2 S = pack2(__uint_as_float(0x3f800000u - (__float_as_uint(t0) << 23)),
-                       __uint_as_float(0x3f800000u - (__float_as_uint(t1) << 23)));
-    const f2 Sp = mul2(S, p);
-    a = add2(S, Sp);
-    m = add2(add2(splat2(1.0f), neg2(S)), neg2(Sp));
+    const f2 S = pack2(__uint_as_float(__float_as_uint(t0) * 0xff800000u + 0x3f800000u),  // 2^-j
+                       __uint_as_float(__float_as_uint(t1) * 0xff800000u + 0x3f800000u));
+    a = fma2(S, p, S);
+    m = fma2(S, mul2(p, splat2(-1.0f)), minus2(splat2(1.0f), S));
 }
 
 // Two tokens' or channels' decay a and input b = beta sigmoid(ig) x.  cl: rate log2 e.
@@ -89,8 +98,8 @@ __device__ __forceinline__ void token2(f2 x, f2 g, f2 ig, f2 cl, f2 &a, f2 &b) {
     if constexpr (DECAY) {
         f2 m;
         decay2(rcp2(one_plus_exp(g)), cl, a, m);
-        const f2 w = mul2(m, add2(splat2(2.0f), neg2(m)));
-        f2 v = add2(w, splat2(kTiny));  // w = 0 (a = 1) gives beta = 0, not 0 * inf
+        const f2 r = minus2(splat2(2.0f), m), w = mul2(m, r);
+        f2 v = fma2(m, r, splat2(kTiny));  // w = 0 (a = 1) gives beta = 0, not 0 * inf
         // beta sigmoid(ig) = sqrt(w) / (1 + E) = w rsqrt(w (1 + E)^2): one MUFU operation
         // for the square root and the quotient
         if constexpr (IG) {
@@ -107,11 +116,11 @@ __device__ __forceinline__ void token2(f2 x, f2 g, f2 ig, f2 cl, f2 &a, f2 &b) {
 }
 
 // Two tokens' or channels' factors of the gradients that need no state: with G the whole
-// gradient of h_t,  dx = G px,  dig = G pi,  dgate = G kg (h_{t-1} - v),
-// drate += G kr (h_{t-1} - v):
-//   dh/da = h_{t-1} + u dbeta/da;  no rate: dbeta/da = -1, da/dg = s n: v = u, kg = s n
+// gradient of h_t,  dx = G px,  dig = G pi,  dgate = G kg (v - h_{t-1}),
+// drate += G kr (v - h_{t-1}):
+//   dh/da = h_{t-1} + u dbeta/da;  no rate: dbeta/da = -1, da/dg = s n: v = u, kg = -s n
 //   rate: dbeta/da = -a/beta, da/dz = -a, dz/dc = s, dz/dg = c s n: v = a u / beta,
-//   kr = -s a, kg = kr c n.
+//   kr = s a, kg = kr c n.
 // a/beta diverges as z -> 0, but s a^2/beta -> 0 with it: 1/beta is taken of at least
 // 2^-126, which keeps every product finite and its limit 0.
 template <bool DECAY, bool IG>
@@ -126,18 +135,18 @@ __device__ __forceinline__ void token_grad2(f2 x, f2 g, f2 ig, f2 c, f2 cl, f2 &
     if constexpr (DECAY) {
         f2 m;
         decay2(s, cl, a, m);
-        const f2 w = mul2(m, add2(splat2(2.0f), neg2(m)));
-        const f2 ib = map2(add2(w, splat2(kTiny)), [](float y) { return rsqrt_approx(y); });
+        const f2 r = minus2(splat2(2.0f), m), w = mul2(m, r);
+        const f2 ib = map2(fma2(m, r, splat2(kTiny)), [](float y) { return rsqrt_approx(y); });
         beta = mul2(w, ib);
         v = mul2(mul2(a, ib), u);
-        kr = neg2(mul2(s, a));
+        kr = mul2(s, a);
         kg = mul2(kr, mul2(c, n));
     } else {
         a = s;
         beta = n;
         v = u;
         kr = 0;
-        kg = mul2(s, n);
+        kg = mul2(mul2(s, splat2(-1.0f)), n);
     }
     b = mul2(beta, u);
     px = IG ? mul2(beta, si) : beta;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kStepThreads) glr_step_kernel(const FwdParams 
     IO *y = static_cast<IO *>(p.y) + row0;
     f2 h = 0, cl = 0;
     if (p.h0) h = V == 2 ? pack2(p.h0[i], p.h0[i + V - 1]) : splat2(p.h0[i]);
-    if constexpr (DECAY) cl = mul2(load_channels<float, V>(p.rate + d), splat2(kLog2e));
+    if constexpr (DECAY) cl = mul2(capped_rate(load_channels<float, V>(p.rate + d)), splat2(kLog2e));
     for (int64_t t = 0; t < p.L; ++t) {
         if (p.states && t % kRun == 0)
             store_channels<float, V>(p.states + (b * p.nruns + t / kRun) * p.D + d, h);

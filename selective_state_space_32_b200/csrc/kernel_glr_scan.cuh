@@ -7,7 +7,7 @@
 // and channel group in steps of C W runs:
 //   1. every warp computes a and b of its run (registers) and the run's composition;
 //   2. the block's warps exchange compositions through shared memory, and the cluster's
-//      blocks the blocks' through distributed shared memory (one cluster barrier);
+//      blocks the blocks' through distributed shared memory;
 //   3. every thread applies what precedes its run to the carried state, walks its
 //      tokens once more and stores them; the carried state moves on by the composition
 //      of the whole step, which every block forms for itself in the same order.
@@ -32,6 +32,13 @@ constexpr int kRowBytes = 128;
 constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 8;
 constexpr int kStages = 2;
+#ifndef GLR_K
+#define GLR_K 16
+#endif
+#ifndef GLR_MB
+#define GLR_MB 2
+#endif
+constexpr int kForwardRun = GLR_K;  // tokens of a warp's run; the backward pass takes kRun (a saved state each)
 
 // channels a lane holds
 template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
@@ -39,7 +46,7 @@ template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ?
 template <class IO, bool STAGED, int NS, int K>
 constexpr int scan_smem_bytes(int warps, int cluster) {
     const int ch = 32 * lane_channels<IO, STAGED>();
-    return (STAGED ? warps * kStages * NS * K * kRowBytes : 0) + 2 * (warps + cluster) * ch * 8;
+    return 128 + (STAGED ? warps * kStages * NS * K * kRowBytes : 0) + 2 * (warps + cluster) * ch * 8;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -49,7 +56,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool on) {
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zeros(void *dst, const void *src, bool on) {
     const int n = on ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
 }
@@ -110,14 +120,24 @@ struct RunLoader {
         if constexpr (STAGED) {
             if (t0 >= 0 && t0 < L) {
                 const int col = (lane & 7) * (16 / Io<IO>::kBytes), row = lane >> 3;
-                const int n = col < live ? (L - t0 < K ? static_cast<int>(L - t0) : K) : 0;
-                const int64_t at = t0 * D + row * D + col;
+                const int64_t at = (t0 + row) * D + col, next = 4 * D;
+                unsigned char *dst = ring + stage * kStageBytes + row * kRowBytes + (lane & 7) * 16;
+                if (live == CH && t0 + K <= L) {
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
+                    for (int s = 0; s < NS; ++s) {
+                        const IO *p = src[s] + at;
 #pragma unroll
-                    for (int h = 0; h < K / 4; ++h)
-                        cp_async16(ring + stage * kStageBytes + (s * K + row + 4 * h) * kRowBytes + (lane & 7) * 16,
-                                   row + 4 * h < n ? src[s] + at + 4 * h * D : src[s], row + 4 * h < n);
+                        for (int h = 0; h < K / 4; ++h, p += next) cp_async16(dst + (s * K + 4 * h) * kRowBytes, p);
+                    }
+                } else {
+                    const int n = col < live ? (L - t0 < K ? static_cast<int>(L - t0) : K) : 0;
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int h = 0; h < K / 4; ++h)
+                            cp_async16_or_zeros(dst + (s * K + 4 * h) * kRowBytes,
+                                                row + 4 * h < n ? src[s] + at + h * next : src[s], row + 4 * h < n);
+                }
             }
             cp_async_commit();
         }
@@ -154,37 +174,93 @@ __device__ __forceinline__ void store_map(float2 *p, float a, float h) { *p = ma
 __device__ __forceinline__ void store_map(float2 *p, f2 a, f2 h) {
     *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(a, h);
 }
-// The same at the address that `local` (shared memory of this block) has in block `rank`.
+// The address that `local` (shared memory of this block) has in block `rank`.
 __device__ __forceinline__ uint32_t cluster_address(const void *local, uint32_t rank) {
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
     return at;
 }
-__device__ __forceinline__ void send_map(float2 *local, uint32_t rank, float a, float h) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_address(local, rank)), "f"(a), "f"(h) : "memory");
+// Store a lane's maps there; their bytes are counted on that block's mbarrier.  (A cluster
+// barrier instead has to fence every thread's earlier stores of outputs first.)
+__device__ __forceinline__ void send_map(float2 *local, uint64_t *bar, uint32_t rank, float a, float h) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                     cluster_address(local, rank)), "f"(a), "f"(h), "r"(cluster_address(bar, rank))
+                 : "memory");
 }
-__device__ __forceinline__ void send_map(float2 *local, uint32_t rank, f2 a, f2 h) {
-    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(cluster_address(local, rank)), "l"(a), "l"(h) : "memory");
+__device__ __forceinline__ void send_map(float2 *local, uint64_t *bar, uint32_t rank, f2 a, f2 h) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+                     cluster_address(local, rank)), "l"(a), "l"(h), "r"(cluster_address(bar, rank))
+                 : "memory");
+}
+// mbar_wait for bytes that other blocks of the cluster stored
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
 }
 
-// The exchange of one step.  In: the composition (A, H) of this warp's run, the state
+// What the blocks and warps of a cluster share in a walk: agg [2][warps][CH] and
+// cl [2][C][CH] maps and two mbarriers, used in turn by the steps.  A step's entries are
+// overwritten two steps later: by then this block's warps have met at the step between
+// them, and a block sends its second next maps only after it has this block's next ones,
+// which this block's warps send after that meeting.
+struct Shared {
+    float2 *agg, *cl;
+    uint64_t *bar;
+    uint32_t C, rank;
+    int warps, w, lane;
+    bool lost;  // a wait for the cluster's maps gave up: the state is NaN from there on
+
+    __device__ __forceinline__ void init(unsigned char *smem, unsigned char *maps, int ch, uint32_t cluster) {
+        C = cluster;
+        rank = C > 1 ? cluster_rank() : 0;
+        lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        bar = reinterpret_cast<uint64_t *>(smem);
+        agg = reinterpret_cast<float2 *>(maps);
+        cl = agg + 2 * warps * ch;
+        lost = false;
+        if (C > 1) {
+            if (threadIdx.x == 0) {
+                for (int k = 0; k < 2; ++k) mbar_init(bar + k, 1), mbar_expect_tx(bar + k, C * ch * 8);
+                mbar_fence_init();
+            }
+            __syncwarp();
+            cluster_arrive();
+        }
+    }
+    // Every block of the cluster has started and set up its mbarriers: it may be sent to.
+    __device__ __forceinline__ void start() const {
+        __syncwarp();
+        if (C > 1) cluster_wait();
+    }
+};
+
+// The exchange of step `it`.  In: the composition (A, H) of this warp's run, the state
 // `carry` before the step.  Returns the state before the run; `carry` becomes the state
-// after the step.  agg: [2][warps][CH], cl: [2][C][CH] maps; `par` alternates, so that a
-// step's entries are overwritten only after a barrier that follows their last reading.
+// after the step.
 template <int V>
 __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, typename Lane<V>::T H,
-                                                        typename Lane<V>::T &carry, float2 *agg, float2 *cl, int par,
-                                                        int warps, int w, uint32_t C, uint32_t rank, int lane) {
+                                                        typename Lane<V>::T &carry, Shared &sh, int64_t it) {
     using LV = Lane<V>;
     using T = typename LV::T;
     constexpr int CH = 32 * V;
-    const float2 *at = agg + par * warps * CH + lane * V;
+    const int par = static_cast<int>(it & 1), w = sh.w, warps = sh.warps;
+    const float2 *at = sh.agg + par * warps * CH + sh.lane * V;
     __syncwarp();
     if (warps > 1) {
-        store_map(agg + (par * warps + w) * CH + lane * V, A, H);
+        store_map(sh.agg + (par * warps + w) * CH + sh.lane * V, A, H);
         __syncthreads();
     }
-    if (C == 1) {
+    if (sh.C == 1) {
         if (warps == 1) {
             const T h = carry;
             carry = LV::fma(A, carry, H);
@@ -209,7 +285,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
         Hb = LV::fma(ma, Hb, mh);
     }
     const T Ap = Ab, Hp = Hb;
-    if (static_cast<uint32_t>(w) < C) {
+    if (static_cast<uint32_t>(w) < sh.C) {
         if (warps == 1) {
             Ab = A, Hb = H;
         } else {
@@ -220,17 +296,20 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
                 Hb = LV::fma(ma, Hb, mh);
             }
         }
-        for (uint32_t r = w; r < C; r += warps) send_map(cl + (par * C + rank) * CH + lane * V, r, Ab, Hb);
-        __syncwarp();
+        for (uint32_t r = w; r < sh.C; r += warps)
+            send_map(sh.cl + (par * sh.C + sh.rank) * CH + sh.lane * V, sh.bar + par, r, Ab, Hb);
     }
-    cluster_arrive();
-    cluster_wait();
-    at = cl + par * C * CH + lane * V;
+    if (!sh.lost && !mbar_wait_cluster(sh.bar + par, static_cast<uint32_t>(it >> 1) & 1)) {
+        sh.lost = true;
+        carry = LV::splat(__uint_as_float(0x7fc00000u));
+    }
+    if (threadIdx.x == 0) mbar_expect_tx(sh.bar + par, sh.C * CH * 8);  // for the second next step
+    at = sh.cl + par * sh.C * CH + sh.lane * V;
     T h = carry;
-    for (uint32_t r = 0; r < C; ++r, at += CH) {
+    for (uint32_t r = 0; r < sh.C; ++r, at += CH) {
         T ma, mh;
         load_map(at, ma, mh);
-        if (r == rank) h = carry;
+        if (r == sh.rank) h = carry;
         carry = LV::fma(ma, carry, mh);
     }
     return LV::fma(Ap, h, Hp);
@@ -238,7 +317,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
 
 // grid: B * groups * C blocks of 32 W threads in clusters of C
 template <class IO, bool STAGED, bool DECAY, bool IG, int K>
-__global__ void __launch_bounds__(32 * kMaxWarps, K == 8 ? 3 : 2) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
+__global__ void __launch_bounds__(32 * kMaxWarps, GLR_MB) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 3 : 2;
     using Loader = RunLoader<IO, STAGED, NS, K>;
     constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
@@ -246,15 +325,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, K == 8 ? 3 : 2) glr_scan_kerne
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    if (C > 1) cluster_arrive();
+    Shared sh;
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
+    const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;
     Loader in;
     in.src[0] = static_cast<const IO *>(p.x) + row0;
     in.src[1] = static_cast<const IO *>(p.gate) + row0;
     if constexpr (IG) in.src[2] = static_cast<const IO *>(p.igate) + row0;
-    in.ring = smem + w * kStages * Loader::kStageBytes;
+    in.ring = smem + 128 + w * kStages * Loader::kStageBytes;
     in.L = p.L, in.D = p.D, in.lane = lane;
     in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
     const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
@@ -262,22 +342,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, K == 8 ? 3 : 2) glr_scan_kerne
     const int64_t steps = (p.L + step - 1) / step;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) in.issue(t0 + s * step, s);
-    float2 *agg = reinterpret_cast<float2 *>(smem + (STAGED ? warps * kStages * Loader::kStageBytes : 0));
-    float2 *cl = agg + 2 * warps * CH;
     const bool mine = lane * V < in.live;
     T carry = LV::splat(0.0f);
     f2 cc = 0;  // rate log2 e of the pair
     if (mine) {
-        if constexpr (DECAY) {
-            if constexpr (V == 2) cc = mul2(LV::load(p.rate + ch0 + lane * V), splat2(kLog2e));
-            else cc = splat2(p.rate[ch0 + lane] * kLog2e);
-        }
+        if constexpr (DECAY) cc = mul2(capped_rate(load_channels<float, V>(p.rate + ch0 + lane * V)), splat2(kLog2e));
         if (p.h0) carry = LV::load(p.h0 + b * p.D + ch0 + lane * V);
     }
     IO *y = static_cast<IO *>(p.y) + row0 + lane * V;
     float *states = p.states ? p.states + b * p.nruns * p.D + ch0 + lane * V : nullptr;
-    __syncwarp();
-    if (C > 1) cluster_wait();  // every block of the cluster has started: its shared memory may be written
+    sh.start();
     int stage = 0;
     for (int64_t it = 0; it < steps; ++it, t0 += step) {
         const int n = t0 >= p.L ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
@@ -306,15 +380,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, K == 8 ? 3 : 2) glr_scan_kerne
         __syncwarp();
         in.issue(t0 + kStages * step, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
-        T h = exchange<V>(A, H, carry, agg, cl, static_cast<int>(it & 1), warps, w, C, rank, lane);
-        if (mine) {
+        T h = exchange<V>(A, H, carry, sh, it);
+        IO *yt = y + t0 * p.D;
+        auto emit = [&](int k) {
+            if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D, h);
+            h = LV::fma(LV::get(a, k), h, LV::get(bb, k));
+            store_lane<IO>(yt, h);
+            yt += p.D;
+        };
+        if (mine && n == K) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (k >= n) break;
-                if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D, h);
-                h = LV::fma(LV::get(a, k), h, LV::get(bb, k));
-                store_lane<IO>(y + (t0 + k) * p.D, h);
-            }
+            for (int k = 0; k < K; ++k) emit(k);
+        } else if (mine) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k < n) emit(k);
         }
     }
     if (p.h_final && rank == 0 && w == 0 && mine) LV::store(p.h_final + b * p.D + ch0 + lane * V, carry);
@@ -331,8 +411,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    if (C > 1) cluster_arrive();
+    Shared sh;
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
+    const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;
     Loader in;
@@ -340,7 +421,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
     in.src[1] = static_cast<const IO *>(p.gate) + row0;
     in.src[2] = static_cast<const IO *>(p.dy) + row0;
     if constexpr (IG) in.src[3] = static_cast<const IO *>(p.igate) + row0;
-    in.ring = smem + w * kStages * Loader::kStageBytes;
+    in.ring = smem + 128 + w * kStages * Loader::kStageBytes;
     in.L = p.L, in.D = p.D, in.lane = lane;
     in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
     const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
@@ -348,22 +429,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
     const int64_t steps = (p.nruns * K + step - 1) / step;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) in.issue(t0 - s * step, s);
-    float2 *agg = reinterpret_cast<float2 *>(smem + (STAGED ? warps * kStages * Loader::kStageBytes : 0));
-    float2 *cl = agg + 2 * warps * CH;
     const bool mine = lane * V < in.live;
     T carry = LV::splat(0.0f), dc = LV::splat(0.0f);
     f2 cn = 0, cl2 = 0;  // the pair's rate, and rate log2 e
     if (mine) {
         if constexpr (DECAY) {
-            if constexpr (V == 2) cn = LV::load(p.rate + ch0 + lane * V);
-            else cn = splat2(p.rate[ch0 + lane]);
+            cn = capped_rate(load_channels<float, V>(p.rate + ch0 + lane * V));
             cl2 = mul2(cn, splat2(kLog2e));
         }
         if (p.dh_final) carry = LV::load(p.dh_final + b * p.D + ch0 + lane * V);
     }
     const int64_t out0 = row0 + lane * V;
-    __syncwarp();
-    if (C > 1) cluster_wait();
+    sh.start();
     int stage = 0;
     for (int64_t it = 0; it < steps; ++it, t0 -= step) {
         const int n = t0 < 0 ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
@@ -382,28 +459,24 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
                 token_grad2<DECAY, IG>(in.pair(t0, n, stage, 0, i), in.pair(t0, n, stage, 1, i),
                                        IG ? in.pair(t0, n, stage, NS - 1, i) : 0, cn, cl2, a[i], bb, v, px[i], pi[i], kg, kr);
                 if constexpr (V == 2) {
-                    d = add2(h, neg2(v));
+                    d = minus2(v, h);
                     h = fma2(a[i], h, bb);
                 } else {  // two tokens of one channel: the second's state follows from the first's
                     float a0, a1, b0, b1;
                     unpack2(a[i], a0, a1);
                     unpack2(bb, b0, b1);
                     const float h1 = fmaf(a0, h, b0);
-                    d = add2(pack2(h, h1), neg2(v));
+                    d = minus2(v, pack2(h, h1));
                     h = fmaf(a1, h1, b1);
                 }
                 pg[i] = mul2(kg, d);
                 pr[i] = mul2(kr, d);
             }
         }
-        if (n < K) {  // tokens past the end: the identity (and no part in the rate's sum)
+        if (n < K) {  // tokens past the end: the identity
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (k >= n) {
-                    LV::set(a, k, LV::splat(1.0f));
-                    LV::set(g, k, LV::splat(0.0f));
-                    if constexpr (DECAY) LV::set(pr, k, LV::splat(0.0f));
-                }
+                if (k >= n) LV::set(a, k, LV::splat(1.0f)), LV::set(g, k, LV::splat(0.0f));
         }
         T A = LV::splat(1.0f), F = LV::splat(0.0f);
 #pragma unroll
@@ -414,23 +487,30 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
         __syncwarp();
         in.issue(t0 - kStages * step, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
-        T e = exchange<V>(A, F, carry, agg, cl, static_cast<int>(it & 1), warps, w, C, rank, lane);
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k) {
+        T e = exchange<V>(A, F, carry, sh, it);
+        const int64_t at = out0 + t0 * p.D;
+        IO *dx = static_cast<IO *>(p.dx) + at, *dg = static_cast<IO *>(p.dgate) + at;
+        IO *di = IG ? static_cast<IO *>(p.digate) + at : nullptr;
+        auto emit = [&](int k) {
             const T G = LV::add(LV::get(g, k), e);
             e = LV::mul(LV::get(a, k), G);
             if constexpr (DECAY) dc = LV::fma(G, LV::get(pr, k), dc);
-            if (mine && k < n) {
-                const int64_t at = out0 + (t0 + k) * p.D;
-                store_lane<IO>(static_cast<IO *>(p.dx) + at, LV::mul(G, LV::get(px, k)));
-                store_lane<IO>(static_cast<IO *>(p.dgate) + at, LV::mul(G, LV::get(pg, k)));
-                if constexpr (IG) store_lane<IO>(static_cast<IO *>(p.digate) + at, LV::mul(G, LV::get(pi, k)));
-            }
+            store_lane<IO>(dx + k * p.D, LV::mul(G, LV::get(px, k)));
+            store_lane<IO>(dg + k * p.D, LV::mul(G, LV::get(pg, k)));
+            if constexpr (IG) store_lane<IO>(di + k * p.D, LV::mul(G, LV::get(pi, k)));
+        };
+        if (mine && n == K) {
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k) emit(k);
+        } else if (mine) {
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k)
+                if (k < n) emit(k);
         }
     }
     if (p.dh0 && rank == 0 && w == 0 && mine) LV::store(p.dh0 + b * p.D + ch0 + lane * V, carry);
     if constexpr (DECAY) {
-        float *sums = reinterpret_cast<float *>(agg);  // [warps][CH], once the last step's entries are read
+        float *sums = reinterpret_cast<float *>(sh.agg);  // [warps][CH], once the last step's entries are read
         __syncthreads();
         LV::store(sums + w * CH + lane * V, dc);
         __syncthreads();

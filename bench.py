@@ -69,7 +69,7 @@ SSD_SOURCES = ("kernel_ssd.cuh", "ssd.cu")
 HOST_ONLY_SOURCES = ("host_pipe.cu",)  # copies and sub-plan calls: no kernel launch of its own
 # the recurrent block's other operators, whose kernels no workload here launches
 BLOCK_SOURCES = ("abi_checks.cuh", "column_sums.cuh", "glr.cu", "glr_math.cuh", "kernel_glr.cuh",
-                 "kernel_norm.cuh", "norm.cu")
+                 "kernel_glr_scan.cuh", "kernel_norm.cuh", "norm.cu")
 
 
 def kernel_sources_hash(read=None, family: str = "scan") -> str:

@@ -3,9 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
-#include <cstdio>
-#include <cstdlib>
 
 #include "abi_checks.cuh"
 #include "column_sums.cuh"
@@ -22,33 +21,64 @@ int check_sizes(int64_t B, int64_t L, int64_t D, int dtype) {
     if (B < 1 || D < 1 || L < 0) return SSCAN_ERR_INVALID;
     if (dtype != SSCAN_F32 && dtype != SSCAN_BF16) return SSCAN_ERR_INVALID;
     const int64_t kMax = int64_t(1) << 31;
-    if (B >= kMax || D >= kMax || B * D >= kMax) return SSCAN_ERR_UNSUPPORTED;
+    if (B >= kMax || D > (int64_t(1) << 28) || B * D >= kMax) return SSCAN_ERR_UNSUPPORTED;
     if (L > (int64_t(1) << 40) || (L > 0 && B * D > (int64_t(1) << 48) / L)) return SSCAN_ERR_UNSUPPORTED;
     return SSCAN_OK;
 }
 
+// Up to this many tokens the forward pass takes one thread per channel pair: 128 rows of 8
+// tokens, 2048 channels 5.8 us against 10.9 of the scan; 16 tokens of 8 rows 4.8 against 2.9.
+constexpr int64_t kStepTokens = 8;
+
 int64_t runs(int64_t L) { return ceil_div(L, glr::kRun); }
 
-// How a scan is spread: warps of a block and blocks of a cluster along the sequence, or
-// (warps = 0) one thread per channel.
+// How a walk is spread along the sequence: warps of a block, blocks of a cluster.
 struct Shape {
     int warps, cluster;
 };
 
-Shape scan_shape(int64_t B, int64_t L, int64_t D, int ch) {
-#ifdef GLR_TUNE
-    if (const char *e = getenv("GLR_TUNE")) { Shape s; int w, c; if (sscanf(e, "%d,%d", &w, &c) == 2) return Shape{w, c}; }
-#endif
-    if (L <= 4) return {0, 1};
-    const int64_t n = runs(L), chains = B * ceil_div(D, ch);
-    int w = 1, c = 1;
-    while (w < glr::kMaxWarps && w < n) w *= 2;
-    while (c < glr::kMaxCluster && c * w < n && chains * c * w < 148 * 16) c *= 2;
+// `chains` = batch rows times channel groups, `n` = runs of the sequence.  Measured on B200
+// (us; warps x blocks): about ten warps an SM are wanted, in small blocks first: 192 chains
+// of 2048 tokens, bf16 with rate and input gate: 4x2 54, 4x1 74, 8x4 58; 384 fp32 chains:
+// 4x1 49, 8x1 56, 4x2 56; 128 chains of 8192 tokens: 4x4 81, 4x2 95, 8x8 105.  Where that
+// leaves the device half empty, blocks of 8 warps (32 chains of 131072 tokens: 8x8 621, 4x8
+// 632, backward 1135 against 1422), and for a handful of chains clusters of 16 (1 chain of
+// 65536 tokens: 8x16 95, 8x8 205).  With very many chains fewer warps share one: 2048 chains
+// of 32 tokens, backward: 2x1 19.7, 4x1 21.0.
+Shape scan_shape(int64_t chains, int64_t n) {
+    constexpr int64_t kWant = 148 * 10;
+    int w = 1;
+    while (w < 4 && w < n) w *= 2;
+    while (w > 1 && chains * w >= 8192) w /= 2;
+    auto cluster = [&](int most) {
+        int c = 1;
+        while (c < most && c * w < n && chains * w * c < kWant) c *= 2;
+        return c;
+    };
+    int c = cluster(8);
+    if (w * c < n && chains * w * c < kWant) w = glr::kMaxWarps, c = cluster(8);
+    if (w * c < n && chains * w * c < kWant / 4) c = cluster(glr::kMaxCluster);
     return {w, c};
 }
 
 template <class IO>
 bool staged(int64_t D) { return D * int64_t(sizeof(IO)) % 16 == 0; }
+
+// Dynamic shared memory, and clusters of more than 8 blocks, for kernel KERN: once per
+// (kernel, device) as smem_opt_in does.
+template <auto KERN>
+cudaError_t cluster_opt_in(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
 
 // Blocks, cluster and shared memory of a scan kernel's launch, on stream s.
 struct Launch {
@@ -70,18 +100,19 @@ struct Launch {
 template <class IO, bool STAGED, bool DECAY, bool IG>
 int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
     constexpr int NS = IG ? 3 : 2, ch = 32 * glr::lane_channels<IO, STAGED>();
-    const Shape sh = scan_shape(p.B, p.L, p.D, ch);
-    if (sh.warps == 0) {
+    if (p.L <= kStepTokens) {
         constexpr int V = STAGED ? 2 : 1;
         const int64_t blocks = ceil_div(p.B * p.D, V * glr::kStepThreads);
         glr::glr_step_kernel<IO, V, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
         return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
     }
     constexpr int K = glr::kForwardRun;
+    const int64_t groups = ceil_div(p.D, ch);
+    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K));
     constexpr auto kern = glr::glr_scan_kernel<IO, STAGED, DECAY, IG, K>;
-    if (smem_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
+    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
-    const int64_t groups = ceil_div(p.D, ch), blocks = p.B * groups * sh.cluster;
+    const int64_t blocks = p.B * groups * sh.cluster;
     Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, K>(sh.warps, sh.cluster), s);
     return cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) == cudaSuccess ? SSCAN_OK
                                                                                                        : SSCAN_ERR_CUDA;
@@ -95,12 +126,13 @@ int launch_forward(const glr::FwdParams &p, cudaStream_t s) {
 template <class IO, bool STAGED, bool DECAY, bool IG>
 int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
     constexpr int NS = IG ? 4 : 3, ch = 32 * glr::lane_channels<IO, STAGED>();
-    Shape sh = scan_shape(p.B, p.L, p.D, ch);
-    if (sh.warps == 0) sh.warps = 1;
+    const int64_t groups = ceil_div(p.D, ch);
+    const Shape sh = scan_shape(p.B * groups, p.nruns);
     constexpr auto kern = glr::glr_scan_backward_kernel<IO, STAGED, DECAY, IG>;
-    if (smem_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
+    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(glr::kMaxWarps, glr::kMaxCluster)) !=
+        cudaSuccess)
         return SSCAN_ERR_CUDA;
-    const int64_t groups = ceil_div(p.D, ch), blocks = p.B * groups * sh.cluster;
+    const int64_t blocks = p.B * groups * sh.cluster;
     Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(sh.warps, sh.cluster), s);
     if (cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) != cudaSuccess) return SSCAN_ERR_CUDA;
     if (!DECAY) return SSCAN_OK;

@@ -30,15 +30,9 @@ namespace glr {
 
 constexpr int kRowBytes = 128;
 constexpr int kMaxWarps = 8;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // above 8 is not portable between devices; this one has 16
 constexpr int kStages = 2;
-#ifndef GLR_K
-#define GLR_K 16
-#endif
-#ifndef GLR_MB
-#define GLR_MB 2
-#endif
-constexpr int kForwardRun = GLR_K;  // tokens of a warp's run; the backward pass takes kRun (a saved state each)
+constexpr int kForwardRun = 16;  // tokens of a warp's run; the backward pass takes kRun (a saved state each)
 
 // channels a lane holds
 template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
@@ -65,6 +59,10 @@ __device__ __forceinline__ void cp_async16_or_zeros(void *dst, const void *src, 
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The warp's index, known to the compiler to be the same in its lanes (row addresses are
+// then formed once a warp)
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
 
 // A lane's V channels: one value, or a packed pair.
 template <int V> struct Lane;
@@ -120,14 +118,15 @@ struct RunLoader {
         if constexpr (STAGED) {
             if (t0 >= 0 && t0 < L) {
                 const int col = (lane & 7) * (16 / Io<IO>::kBytes), row = lane >> 3;
-                const int64_t at = (t0 + row) * D + col, next = 4 * D;
+                const uint32_t own = row * D + col;  // 3 D at most: D is below 2^28 where rows are staged
+                const int64_t next = 4 * D;
                 unsigned char *dst = ring + stage * kStageBytes + row * kRowBytes + (lane & 7) * 16;
                 if (live == CH && t0 + K <= L) {
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
-                        const IO *p = src[s] + at;
+                        const IO *p = src[s] + t0 * D;
 #pragma unroll
-                        for (int h = 0; h < K / 4; ++h, p += next) cp_async16(dst + (s * K + 4 * h) * kRowBytes, p);
+                        for (int h = 0; h < K / 4; ++h, p += next) cp_async16(dst + (s * K + 4 * h) * kRowBytes, p + own);
                     }
                 } else {
                     const int n = col < live ? (L - t0 < K ? static_cast<int>(L - t0) : K) : 0;
@@ -136,7 +135,7 @@ struct RunLoader {
 #pragma unroll
                         for (int h = 0; h < K / 4; ++h)
                             cp_async16_or_zeros(dst + (s * K + 4 * h) * kRowBytes,
-                                                row + 4 * h < n ? src[s] + at + h * next : src[s], row + 4 * h < n);
+                                                row + 4 * h < n ? src[s] + t0 * D + h * next + own : src[s], row + 4 * h < n);
                 }
             }
             cp_async_commit();
@@ -223,7 +222,7 @@ struct Shared {
     __device__ __forceinline__ void init(unsigned char *smem, unsigned char *maps, int ch, uint32_t cluster) {
         C = cluster;
         rank = C > 1 ? cluster_rank() : 0;
-        lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
         bar = reinterpret_cast<uint64_t *>(smem);
         agg = reinterpret_cast<float2 *>(maps);
         cl = agg + 2 * warps * ch;
@@ -317,14 +316,14 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
 
 // grid: B * groups * C blocks of 32 W threads in clusters of C
 template <class IO, bool STAGED, bool DECAY, bool IG, int K>
-__global__ void __launch_bounds__(32 * kMaxWarps, GLR_MB) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 3 : 2;
     using Loader = RunLoader<IO, STAGED, NS, K>;
     constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
     using LV = Lane<V>;
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
     sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
     const uint32_t rank = sh.rank;
@@ -349,8 +348,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, GLR_MB) glr_scan_kernel(const 
         if constexpr (DECAY) cc = mul2(capped_rate(load_channels<float, V>(p.rate + ch0 + lane * V)), splat2(kLog2e));
         if (p.h0) carry = LV::load(p.h0 + b * p.D + ch0 + lane * V);
     }
-    IO *y = static_cast<IO *>(p.y) + row0 + lane * V;
-    float *states = p.states ? p.states + b * p.nruns * p.D + ch0 + lane * V : nullptr;
+    IO *y = static_cast<IO *>(p.y) + row0;
+    const uint32_t own = lane * V;
+    float *states = p.states ? p.states + b * p.nruns * p.D + ch0 : nullptr;
     sh.start();
     int stage = 0;
     for (int64_t it = 0; it < steps; ++it, t0 += step) {
@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, GLR_MB) glr_scan_kernel(const 
         T h = exchange<V>(A, H, carry, sh, it);
         IO *yt = y + t0 * p.D;
         auto emit = [&](int k) {
-            if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D, h);
+            if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D + own, h);
             h = LV::fma(LV::get(a, k), h, LV::get(bb, k));
-            store_lane<IO>(yt, h);
+            store_lane<IO>(yt + own, h);
             yt += p.D;
         };
         if (mine && n == K) {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
     using LV = Lane<V>;
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
     sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
     const uint32_t rank = sh.rank;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
         }
         if (p.dh_final) carry = LV::load(p.dh_final + b * p.D + ch0 + lane * V);
     }
-    const int64_t out0 = row0 + lane * V;
+    const uint32_t own = lane * V;
     sh.start();
     int stage = 0;
     for (int64_t it = 0; it < steps; ++it, t0 -= step) {
@@ -488,16 +488,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(co
         in.issue(t0 - kStages * step, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
         T e = exchange<V>(A, F, carry, sh, it);
-        const int64_t at = out0 + t0 * p.D;
+        const int64_t at = row0 + t0 * p.D;
         IO *dx = static_cast<IO *>(p.dx) + at, *dg = static_cast<IO *>(p.dgate) + at;
         IO *di = IG ? static_cast<IO *>(p.digate) + at : nullptr;
         auto emit = [&](int k) {
             const T G = LV::add(LV::get(g, k), e);
             e = LV::mul(LV::get(a, k), G);
             if constexpr (DECAY) dc = LV::fma(G, LV::get(pr, k), dc);
-            store_lane<IO>(dx + k * p.D, LV::mul(G, LV::get(px, k)));
-            store_lane<IO>(dg + k * p.D, LV::mul(G, LV::get(pg, k)));
-            if constexpr (IG) store_lane<IO>(di + k * p.D, LV::mul(G, LV::get(pi, k)));
+            store_lane<IO>(dx + k * p.D + own, LV::mul(G, LV::get(px, k)));
+            store_lane<IO>(dg + k * p.D + own, LV::mul(G, LV::get(pg, k)));
+            if constexpr (IG) store_lane<IO>(di + k * p.D + own, LV::mul(G, LV::get(pi, k)));
         };
         if (mine && n == K) {
 #pragma unroll

@@ -6,7 +6,7 @@
 
 namespace sscan {
 
-constexpr int kColThreads = 256;  // 32 channels x 8 row lanes
+constexpr int kColThreads = 1024;  // 32 channels x 32 row lanes
 
 // part [rows][D] fp32; grid.x = ceil(D / 32), grid.y = planes: plane k reads
 // part + k * plane_stride and writes outs[k] (null: skipped).
@@ -17,7 +17,7 @@ struct ColumnSums {
 };
 
 static __global__ void __launch_bounds__(kColThreads) column_sums_kernel(const ColumnSums p) {
-    __shared__ float sm[8][32];
+    __shared__ float sm[32][33];
     float *out = blockIdx.y == 0 ? p.out[0] : p.out[1];
     if (out == nullptr) return;  // the same for the whole block
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -26,22 +26,22 @@ static __global__ void __launch_bounds__(kColThreads) column_sums_kernel(const C
     float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
     if (d < p.D) {
         int64_t r = w;
-        for (; r + 24 < p.rows; r += 32) {
+        for (; r + 96 < p.rows; r += 128) {
             s0 += part[r * p.D + d];
-            s1 += part[(r + 8) * p.D + d];
-            s2 += part[(r + 16) * p.D + d];
-            s3 += part[(r + 24) * p.D + d];
+            s1 += part[(r + 32) * p.D + d];
+            s2 += part[(r + 64) * p.D + d];
+            s3 += part[(r + 96) * p.D + d];
         }
-        for (; r < p.rows; r += 8) s0 += part[r * p.D + d];
+        for (; r < p.rows; r += 32) s0 += part[r * p.D + d];
     }
     sm[w][lane] = (s0 + s1) + (s2 + s3);
     __syncthreads();
-    if (w == 0 && d < p.D) {
-        float s = 0.0f;
+    // warp w joins the 32 sums of channel w of the block's 32, by a tree
+    float s = sm[lane][w];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += sm[k][lane];
-        out[d] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 32 + w;
+    if (lane == 0 && e < p.D) out[e] = s;
 }
 
 }  // namespace sscan

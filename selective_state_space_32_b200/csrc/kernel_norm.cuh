@@ -8,16 +8,26 @@
 //   dw = sum over rows of dy z,  db = sum over rows of dy
 //
 // Statistics are of the rounded s, the value that the residual stream holds and that the
-// backward pass reads; they are taken in two passes (mean, then the centred squares) in
-// fp32, so that a mean far from zero costs no digits of the variance.
+// backward pass reads.  They come from centred squares, so that a mean far from zero costs
+// no digits of the variance.
+//
+// Both passes are streams: a row is read once, held in registers, and written once.  T
+// threads share a row, in vectors of VE consecutive values (16 bytes of x, or single
+// values where D is not a multiple), NV vectors a thread: thread i takes vectors i, i + T,
+// ...  A short row belongs to a group of G = 8, 16 or 32 lanes (no barrier at all); a longer
+// one is the block's (G = 0), which meets once: each warp reduces its own part (forward: mean and centred squares,
+// joined by (n, mean, M2) as of sets; backward: two sums), and every thread joins the
+// warps' results in the same order.
+//
+// The backward pass's blocks stay and walk the rows, so that a thread keeps its columns'
+// dw and db in registers; a block leaves one row of partial sums, and the next rows'
+// inputs are in flight while a row is worked on.
 #pragma once
 
 #include "device_utils.cuh"
 
 namespace sscan {
 namespace norm {
-
-constexpr int kRowThreads = 256;
 
 struct FwdParams {
     const void *x, *residual;
@@ -26,29 +36,400 @@ struct FwdParams {
     float *mean, *rstd;
     int64_t rows, D;
     float eps;
+    int rms;
 };
 
 struct BwdParams {
     const void *dy, *s, *dresidual;
     const float *mean, *rstd, *weight;
     void *ds, *dx;  // ds in s's type; dx in dy's type (null: the same type, ds serves)
-    float *part;    // [2][parts][D]: dw, db of each block's rows
+    float *part;    // [2][gridDim.x][D]: dw, db of each block's rows
     int64_t rows, D;
-    int want_dw, want_db;
+    int rms, want_dw, want_db;
 };
 
-__device__ __forceinline__ float rsqrt_fp32(float v) { return 1.0f / sqrtf(v); }
+constexpr int kMaxThreads = 1024;
 
-// Sum over the block's 256 threads, the same value in every thread (sm: 8 floats; the
-// caller's next use of the same sm comes after another barrier of its own).
-__device__ __forceinline__ float block_sum(float v, float *sm) {
+__device__ __forceinline__ float inv_sqrt(float v) { return 1.0f / sqrtf(v); }
+// Sum over groups of G lanes, the same value in each lane of a group
+template <int G = 32>
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// VE consecutive values of type T as loaded, and as fp32
+template <class T, int VE> struct Raw {
+    static constexpr int kWords = VE * Io<T>::kBytes / 4;  // 0 with VE = 1 of bf16
+    uint32_t w[kWords > 0 ? kWords : 1];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VE == 1) {
+            if constexpr (sizeof(T) == 4) w[0] = __float_as_uint(Io<T>::ld(p));
+            else w[0] = Io<T>::ld(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void load_shared(const void *p) {
+        if constexpr (VE == 1) {
+            if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t *>(p);
+            else w[0] = *reinterpret_cast<const uint16_t *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (uint32_t &x : w) x = 0;
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[VE]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) w[e] = __float_as_uint(v[e]);
+        } else if constexpr (VE == 1) {
+            asm("{\n\t.reg .b16 h;\n\tcvt.rn.bf16.f32 h, %1;\n\tmov.b32 %0, {h, 0};\n\t}" : "=r"(w[0]) : "f"(v[0]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VE; e += 2)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e / 2]) : "f"(v[e + 1]), "f"(v[e]));
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VE == 1) {
+            if constexpr (sizeof(T) == 4) *p = __uint_as_float(w[0]);
+            else *p = static_cast<uint16_t>(w[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+};
+
+// values of a row that warp w of a row of T threads holds
+template <int VE, int NV>
+__device__ __forceinline__ int warp_values(int64_t nvec, int w, int T) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t left = nvec - (w * 32 + static_cast<int64_t>(i) * T);
+        n += left >= 32 ? 32 : left > 0 ? static_cast<int>(left) : 0;
+    }
+    return n * VE;
+}
+
+// IO: x, y; R: residual and residual_out.  G > 0: blockDim / G rows a block; G = 0: one.
+template <class IO, class R, bool RES, int VE, int NV, int G>
+__global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(const FwdParams p) {
+    __shared__ float4 part[32];  // a warp's number of values, their mean and centred squares
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int T = G ? G : blockDim.x, t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
+    const int64_t row = G ? (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / (G ? G : 1) : blockIdx.x;
+    // groups past the last row go along with nothing to read or write
+    const int64_t nvec = row < p.rows ? p.D / VE : 0, at = row * p.D;
+    float v[NV][VE];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t j = t + static_cast<int64_t>(i) * T;
+        Raw<IO, VE> x;
+        x.zero();
+        if (j < nvec) x.load(static_cast<const IO *>(p.x) + at + j * VE);
+        if constexpr (RES) {
+            Raw<R, VE> r;
+            r.zero();
+            if (j < nvec) r.load(static_cast<const R *>(p.residual) + at + j * VE);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] = x.get(e) + r.get(e);
+            r.set(v[i]);
+            if (j < nvec) r.store(static_cast<R *>(p.residual_out) + at + j * VE);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] = r.get(e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] = x.get(e);
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) sum += v[i][e];
+    }
+    const int n = G ? static_cast<int>(p.D) : warp_values<VE, NV>(nvec, w, T);
+    float mu = p.rms || n == 0 ? 0.0f : warp_sum<G ? G : 32>(sum) / static_cast<float>(n);
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (t + static_cast<int64_t>(i) * T < nvec) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sq = fmaf(v[i][e] - mu, v[i][e] - mu, sq);
+        }
+    sq = warp_sum<G ? G : 32>(sq);
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    if constexpr (!G) {
+        if (lane == 0) part[w] = make_float4(static_cast<float>(n), mu, sq, 0.0f);
+        __syncthreads();
+        // lane q takes warp q's part
+        const float4 o = lane < (blockDim.x >> 5) ? part[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        mu = p.rms ? 0.0f : warp_sum(o.x * o.y) * inv_d;
+        const float d = o.y - mu;
+        sq = warp_sum(fmaf(o.x * d, d, o.z));
+    }
+    const float rstd = inv_sqrt(fmaf(sq, inv_d, p.eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t j = t + static_cast<int64_t>(i) * T;
+        if (j >= nvec) continue;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[i][e] = (v[i][e] - mu) * rstd;
+        if (p.weight) {
+            Raw<float, VE> g;
+            g.load(p.weight + j * VE);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] *= g.get(e);
+        }
+        if (p.bias) {
+            Raw<float, VE> g;
+            g.load(p.bias + j * VE);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] += g.get(e);
+        }
+        Raw<IO, VE> o;
+        o.set(v[i]);
+        o.store(static_cast<IO *>(p.y) + at + j * VE);
+    }
+    if (t == 0 && row < p.rows) {
+        if (p.mean) p.mean[row] = mu;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Rows of a ring, a group's or a block's
+template <int G> constexpr int bwd_stages() { return G ? 4 : 2; }
+// Threads of an SM: a thread's sums and its values of the row take about 100 registers
+constexpr int kBwdThreads = 640;
+
+// Bytes of a staged row: dy, s and (with DRES) dresidual
+template <class IO, class R>
+__host__ __device__ constexpr int64_t bwd_row_bytes(int64_t D, bool dres) {
+    return D * (Io<IO>::kBytes + (dres ? 2 : 1) * Io<R>::kBytes);
+}
+
+// A thread's NV VE values of a row as pairs (past the row's end: zeros), from memory or, with
+// `staged`, from shared memory.
+template <class X, int VE, int NV>
+__device__ __forceinline__ void load_pairs(const X *row, const unsigned char *staged, int t, int T, int nvec,
+                                           f2 (&v)[NV * VE / 2]) {
+    Raw<X, VE> q[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int j = t + i * T;
+        q[i].zero();
+        if (j < nvec) {
+            if (staged != nullptr) q[i].load_shared(staged + j * VE * Io<X>::kBytes);
+            else q[i].load(row + j * VE);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NV * VE / 2; ++k)
+        v[k] = pack2(q[2 * k / VE].get(2 * k % VE), q[(2 * k + 1) / VE].get((2 * k + 1) % VE));
+}
+
+// IO: dy, dx; R: s, dresidual, ds.  G > 0: G lanes a row; G = 0: a block a row.  With VE > 1 the
+// rows come through a ring in shared memory, filled by cp.async: every thread copies the
+// vectors that it reads itself, so only its own copies are waited for.  Single values
+// (VE = 1) are loaded from memory; the blocks of an SM cover each other there.  A thread's
+// NV VE values are packed pairs: the pass would be bound by instructions otherwise.
+// Dynamic shared memory: the weight (D floats; ones without a weight), then the rings, used
+// again for the warps' sums (D floats each) at the end.
+template <class IO, class R, int VE, int NV, int G>
+__global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(const BwdParams p) {
+    constexpr bool STAGED = VE > 1;
+    constexpr int kStages = bwd_stages<G>(), NP = NV * VE / 2;
+    __shared__ float2 part[2][32];
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *weight = reinterpret_cast<float *>(smem);
+    unsigned char *ring = smem + (p.D * 4 + 15) / 16 * 16;
+    float *columns = reinterpret_cast<float *>(ring);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int T = G ? G : blockDim.x, t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
+    const int groups = G ? blockDim.x / (G ? G : 1) : 1, group = G ? threadIdx.x / (G ? G : 1) : 0;
+    const int nvec = static_cast<int>(p.D / VE);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    // a warp's groups walk together (their sums are exchanged in one instruction): they end
+    // when the warp's first row is past the last, and a row past it is empty
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t lead = G ? first - (threadIdx.x & 31) / (G ? G : 1) : first;
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    const int64_t row_bytes = bwd_row_bytes<IO, R>(p.D, p.dresidual != nullptr);
+    unsigned char *mine = ring + group * kStages * row_bytes;
+    const int64_t off_s = p.D * Io<IO>::kBytes, off_d = off_s + p.D * Io<R>::kBytes;
+    auto issue = [&](int64_t row, int stage) {
+        if constexpr (STAGED) {
+            if (row < p.rows) {
+                unsigned char *to = mine + stage * row_bytes;
+                const int64_t at = row * p.D;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int j = t + i * T;
+                    if (j >= nvec) continue;
+                    cp_async16(to + j * 16, static_cast<const IO *>(p.dy) + at + j * VE);
+#pragma unroll
+                    for (int h = 0; h < VE * Io<R>::kBytes / 16; ++h) {
+                        const int o = j * VE * Io<R>::kBytes + h * 16;
+                        cp_async16(to + off_s + o, reinterpret_cast<const char *>(static_cast<const R *>(p.s) + at) + o);
+                        if (p.dresidual)
+                            cp_async16(to + off_d + o,
+                                       reinterpret_cast<const char *>(static_cast<const R *>(p.dresidual) + at) + o);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+        if (p.weight) cp_async4(weight + c, p.weight + c);
+        else weight[c] = 1.0f;
+    }
+    cp_async_commit();
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) issue(first + k * step, k);
+    cp_async_wait<kStages>();  // the weight
+    __syncthreads();
+    f2 dw[NP], db[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) dw[k] = db[k] = 0;
+    float mu = 0.0f, r = 0.0f;
+    auto statistics = [&](int64_t row) {
+        if (row < p.rows) mu = p.rms ? 0.0f : __ldg(p.mean + row), r = __ldg(p.rstd + row);
+    };
+    statistics(first);
+    int par = 0, stage = 0;
+    for (int64_t row = first, at0 = lead; at0 < p.rows; row += step, at0 += step, par ^= 1) {
+        const int n = row < p.rows ? nvec : 0;
+        const unsigned char *from = mine + stage * row_bytes;
+        if constexpr (STAGED) cp_async_wait<kStages - 1>();
+        f2 z[NP], v[NP], a = 0, b = 0;
+        load_pairs<R, VE, NV>(static_cast<const R *>(p.s) + row * p.D, STAGED ? from + off_s : nullptr, t, T, n, z);
+        load_pairs<IO, VE, NV>(static_cast<const IO *>(p.dy) + row * p.D, STAGED ? from : nullptr, t, T, n, v);
+        const f2 mm = splat2(-mu), rr = splat2(r);
+        f2 wt[NP];
+        load_pairs<float, VE, NV>(weight, reinterpret_cast<const unsigned char *>(weight), t, T, nvec, wt);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            z[k] = mul2(add2(z[k], mm), rr);
+            dw[k] = fma2(v[k], z[k], dw[k]);
+            db[k] = add2(db[k], v[k]);
+            v[k] = mul2(v[k], wt[k]);
+            a = add2(a, v[k]);
+            b = fma2(v[k], z[k], b);
+        }
+        statistics(row + step);
+        float s1, s2, hi;
+        unpack2(a, s1, hi);
+        s1 = warp_sum<G ? G : 32>(s1 + hi);
+        unpack2(b, s2, hi);
+        s2 = warp_sum<G ? G : 32>(s2 + hi);
+        if constexpr (!G) {
+            if (lane == 0) part[par][w] = make_float2(s1, s2);
+            __syncthreads();  // the other half is written two rows on, after the next meeting
+            const float2 o = lane < warps ? part[par][lane] : make_float2(0.0f, 0.0f);
+            s1 = warp_sum(o.x);
+            s2 = warp_sum(o.y);
+        }
+        const f2 m1 = splat2(p.rms ? 0.0f : -s1 * inv_d), m2 = splat2(-s2 * inv_d);
+        f2 d[NP];
+        if (p.dresidual) {
+            load_pairs<R, VE, NV>(static_cast<const R *>(p.dresidual) + row * p.D, STAGED ? from + off_d : nullptr, t, T,
+                                  n, d);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) d[k] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = t + i * T;
+            float o[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const int k = (i * VE + e) / 2;
+                float lo, up;
+                unpack2(fma2(fma2(z[k], m2, add2(v[k], m1)), rr, d[k]), lo, up);
+                o[e] = (i * VE + e) & 1 ? up : lo;
+            }
+            if (j >= n) continue;
+            Raw<R, VE> q;
+            q.set(o);
+            q.store(static_cast<R *>(p.ds) + row * p.D + j * VE);
+            if (p.dx) {
+                Raw<IO, VE> u;
+                u.set(o);
+                u.store(static_cast<IO *>(p.dx) + row * p.D + j * VE);
+            }
+        }
+        issue(row + kStages * step, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if constexpr (STAGED) cp_async_wait<0>();
+    // the block's partial sums of the columns
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (!(k == 0 ? p.want_dw : p.want_db)) continue;
+        float *out = p.part + (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * p.D;
+        float *own = G ? columns + group * p.D : out;
+        if constexpr (G) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = t + i * T;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const int c = (i * VE + e) / 2;
+                float lo, up;
+                unpack2(k == 0 ? dw[c] : db[c], lo, up);
+                if (j < nvec) own[j * VE + e] = (i * VE + e) & 1 ? up : lo;
+            }
+        }
+        if constexpr (G) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+                float sum = 0.0f;
+                for (int q = 0; q < groups; ++q) sum += columns[q * p.D + c];
+                out[c] = sum;
+            }
+        }
+    }
+}
+
+// Rows too long for the registers of a block: one block a row, in several passes over it.
+constexpr int kLongThreads = 512;
+
+// Sum over the block, the same value in every thread
+__device__ __forceinline__ float block_sum(float v, float *sm) {
+    v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kRowThreads / 32; ++k) s += sm[k];
+    for (int k = 0; k < kLongThreads / 32; ++k) s += sm[k];
     __syncthreads();
     return s;
 }
@@ -62,66 +443,62 @@ __device__ __forceinline__ float load_sum(const IO *x, const R *r, int64_t i) {
     return Io<R>::widen(q);
 }
 
-// IO: x, y; R: residual and residual_out.  One block per row, any D.
-template <class IO, class R, bool RES, bool RMS>
-__global__ void __launch_bounds__(kRowThreads) norm_forward_kernel(const FwdParams p) {
-    __shared__ float sm[kRowThreads / 32];
+template <class IO, class R, bool RES>
+__global__ void __launch_bounds__(kLongThreads) norm_forward_long_kernel(const FwdParams p) {
+    __shared__ float sm[kLongThreads / 32];
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const IO *x = static_cast<const IO *>(p.x) + row * p.D;
-        const R *r = RES ? static_cast<const R *>(p.residual) + row * p.D : nullptr;
-        float mu = 0.0f;
-        if (RES || !RMS) {
-            float v = 0.0f;
-            for (int64_t i = threadIdx.x; i < p.D; i += kRowThreads) {
-                const float s = load_sum<IO, R, RES>(x, r, i);
-                if constexpr (RES) Io<R>::st(static_cast<R *>(p.residual_out) + row * p.D + i, s);
-                v += s;
-            }
-            if constexpr (!RMS) mu = block_sum(v, sm) * inv_d;
-        }
-        float v = 0.0f;
-        for (int64_t i = threadIdx.x; i < p.D; i += kRowThreads) {
-            const float s = load_sum<IO, R, RES>(x, r, i) - mu;
-            v = fmaf(s, s, v);
-        }
-        const float rstd = rsqrt_fp32(block_sum(v, sm) * inv_d + p.eps);
-        for (int64_t i = threadIdx.x; i < p.D; i += kRowThreads) {
-            float o = (load_sum<IO, R, RES>(x, r, i) - mu) * rstd;
-            if (p.weight) o *= __ldg(p.weight + i);
-            if (p.bias) o += __ldg(p.bias + i);
-            Io<IO>::st(static_cast<IO *>(p.y) + row * p.D + i, o);
-        }
-        if (threadIdx.x == 0) {
-            if (p.mean) p.mean[row] = mu;
-            if (p.rstd) p.rstd[row] = rstd;
-        }
+    const int64_t row = blockIdx.x;
+    const IO *x = static_cast<const IO *>(p.x) + row * p.D;
+    const R *r = RES ? static_cast<const R *>(p.residual) + row * p.D : nullptr;
+    float v = 0.0f;
+    for (int64_t i = threadIdx.x; i < p.D; i += kLongThreads) {
+        const float s = load_sum<IO, R, RES>(x, r, i);
+        if constexpr (RES) Io<R>::st(static_cast<R *>(p.residual_out) + row * p.D + i, s);
+        v += s;
+    }
+    const float mu = p.rms ? 0.0f : block_sum(v, sm) * inv_d;
+    v = 0.0f;
+    for (int64_t i = threadIdx.x; i < p.D; i += kLongThreads) {
+        const float s = load_sum<IO, R, RES>(x, r, i) - mu;
+        v = fmaf(s, s, v);
+    }
+    const float rstd = inv_sqrt(block_sum(v, sm) * inv_d + p.eps);
+    for (int64_t i = threadIdx.x; i < p.D; i += kLongThreads) {
+        float o = (load_sum<IO, R, RES>(x, r, i) - mu) * rstd;
+        if (p.weight) o *= __ldg(p.weight + i);
+        if (p.bias) o += __ldg(p.bias + i);
+        Io<IO>::st(static_cast<IO *>(p.y) + row * p.D + i, o);
+    }
+    if (threadIdx.x == 0) {
+        if (p.mean) p.mean[row] = mu;
+        if (p.rstd) p.rstd[row] = rstd;
     }
 }
 
-// IO: dy, dx; R: s, dresidual, ds.  Block k takes rows k, k + gridDim.x, ... and keeps its
-// columns' dw and db in its own rows of part (each entry touched by one thread only).
-template <class IO, class R, bool RMS>
-__global__ void __launch_bounds__(kRowThreads) norm_backward_kernel(const BwdParams p) {
-    __shared__ float sm[kRowThreads / 32];
+// Block k takes rows k, k + gridDim.x, ... and keeps its columns' dw and db in its own rows
+// of part (each entry touched by one thread only).
+template <class IO, class R>
+__global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const BwdParams p) {
+    __shared__ float sm[kLongThreads / 32];
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    float *pw = p.part + blockIdx.x * p.D, *pb = p.part + (gridDim.x + blockIdx.x) * p.D;
+    float *pw = p.part + static_cast<int64_t>(blockIdx.x) * p.D;
+    float *pb = p.part + (static_cast<int64_t>(gridDim.x) + blockIdx.x) * p.D;
     bool first = true;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const IO *dy = static_cast<const IO *>(p.dy) + row * p.D;
         const R *s = static_cast<const R *>(p.s) + row * p.D;
-        const float mu = RMS ? 0.0f : p.mean[row], rstd = p.rstd[row];
+        const float mu = p.rms ? 0.0f : p.mean[row], rstd = p.rstd[row];
         float v1 = 0.0f, v2 = 0.0f;
-        for (int64_t i = threadIdx.x; i < p.D; i += kRowThreads) {
+        for (int64_t i = threadIdx.x; i < p.D; i += kLongThreads) {
             const float z = (Io<R>::widen(Io<R>::ld(s + i)) - mu) * rstd;
             float w = Io<IO>::widen(Io<IO>::ld(dy + i));
             if (p.weight) w *= __ldg(p.weight + i);
             v1 += w;
             v2 = fmaf(w, z, v2);
         }
-        const float m1 = RMS ? 0.0f : block_sum(v1, sm) * inv_d;
+        const float m1 = p.rms ? 0.0f : block_sum(v1, sm) * inv_d;
         const float m2 = block_sum(v2, sm) * inv_d;
-        for (int64_t i = threadIdx.x; i < p.D; i += kRowThreads) {
+        for (int64_t i = threadIdx.x; i < p.D; i += kLongThreads) {
             const float z = (Io<R>::widen(Io<R>::ld(s + i)) - mu) * rstd;
             const float g = Io<IO>::widen(Io<IO>::ld(dy + i));
             const float w = p.weight ? g * __ldg(p.weight + i) : g;

@@ -5,9 +5,11 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "abi_checks.cuh"
 #include "column_sums.cuh"
+#include "device_utils.cuh"
 #include "kernel_norm.cuh"
 #include "sscan.h"
 
@@ -15,40 +17,133 @@ using namespace sscan;
 
 namespace {
 
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
-constexpr int64_t kBwdBlocks = 296;  // backward blocks, each with one row of partial sums per gradient
-
 int check_sizes(int64_t rows, int64_t D, int dtype, uint32_t flags) {
     if (rows < 0 || D < 1) return SSCAN_ERR_INVALID;
     if (dtype != SSCAN_F32 && dtype != SSCAN_BF16) return SSCAN_ERR_INVALID;
     if (flags & ~static_cast<uint32_t>(SSCAN_NORM_RMS | SSCAN_NORM_RESIDUAL_F32)) return SSCAN_ERR_INVALID;
-    if (rows > (int64_t(1) << 40) || D > (int64_t(1) << 31) || (rows > 0 && D > (int64_t(1) << 48) / rows))
-        return SSCAN_ERR_UNSUPPORTED;
+    if (rows >= (int64_t(1) << 31) || D > (int64_t(1) << 28)) return SSCAN_ERR_UNSUPPORTED;  // a block a row at most
     return SSCAN_OK;
 }
 
-int64_t bwd_blocks(int64_t rows) { return rows < kBwdBlocks ? rows : kBwdBlocks; }
+// How a row is shared out: NV vectors of `ve` values a thread, `threads` threads a row (up
+// to 32: groups of lanes; more: a block a row), or nv = 0: too long for registers.
+struct RowShape {
+    int ve, nv, threads;
+};
+RowShape row_shape(int64_t D, int es) {
+    const int ve = D * es % 16 == 0 ? 16 / es : 1;
+    const int64_t n = D / ve;
+    if (ve == 1) {  // single values: 8 a thread
+        if (n <= 256) return {1, 8, 32};
+        if (n <= 8 * norm::kMaxThreads) return {1, 8, static_cast<int>(ceil_div(n, 256) * 32)};
+        return {1, 0, 0};
+    }
+    if (n <= 8) return {ve, 1, 8};
+    if (n <= 16) return {ve, 1, 16};
+    if (n <= 32) return {ve, 1, 32};
+    if (n <= 64) return {ve, 2, 32};
+    if (n <= 128) return {ve, 4, 32};
+    if (es == 4 && n <= 256) return {ve, 8, 32};
+    if (n <= 256) return {ve, 1, static_cast<int>(ceil_div(n, 32) * 32)};
+    if (n <= 1024) return {ve, 2, static_cast<int>(ceil_div(n, 64) * 32)};
+    if (n <= 4 * norm::kMaxThreads) return {ve, 4, static_cast<int>(ceil_div(n, 128) * 32)};
+    return {ve, 0, 0};
+}
+
+template <int N> using Int = std::integral_constant<int, N>;
+
+// f(VE, NV, G) with the shape's constants
+template <int ES, class F>
+int with_shape(const RowShape &sh, F f) {
+    constexpr int V = 16 / ES;
+    const bool group = sh.threads <= 32;
+    if (sh.ve == 1) return group ? f(Int<1>{}, Int<8>{}, Int<32>{}) : f(Int<1>{}, Int<8>{}, Int<0>{});
+    if (sh.threads == 8) return f(Int<V>{}, Int<1>{}, Int<8>{});
+    if (sh.threads == 16) return f(Int<V>{}, Int<1>{}, Int<16>{});
+    if (sh.nv == 1) return group ? f(Int<V>{}, Int<1>{}, Int<32>{}) : f(Int<V>{}, Int<1>{}, Int<0>{});
+    if (sh.nv == 2) return group ? f(Int<V>{}, Int<2>{}, Int<32>{}) : f(Int<V>{}, Int<2>{}, Int<0>{});
+    if (ES == 4 && sh.nv == 8) return f(Int<V>{}, Int<8>{}, Int<32>{});
+    return group ? f(Int<V>{}, Int<4>{}, Int<32>{}) : f(Int<V>{}, Int<4>{}, Int<0>{});
+}
 
 template <class IO, class R, bool RES>
-int launch_forward(const norm::FwdParams &p, bool rms, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(p.rows < kMaxGrid ? p.rows : kMaxGrid);
-    if (rms)
-        norm::norm_forward_kernel<IO, R, RES, true><<<grid, norm::kRowThreads, 0, s>>>(p);
-    else
-        norm::norm_forward_kernel<IO, R, RES, false><<<grid, norm::kRowThreads, 0, s>>>(p);
+int launch_forward(const norm::FwdParams &p, cudaStream_t s) {
+    const RowShape sh = row_shape(p.D, sizeof(IO));
+    if (sh.nv == 0) {
+        norm::norm_forward_long_kernel<IO, R, RES><<<static_cast<unsigned>(p.rows), norm::kLongThreads, 0, s>>>(p);
+    } else {
+        with_shape<sizeof(IO)>(sh, [&](auto ve, auto nv, auto g) {
+            constexpr int rows = g ? 128 / (g ? g : 1) : 1;  // of a block
+            norm::norm_forward_kernel<IO, R, RES, ve, nv, g>
+                <<<static_cast<unsigned>(ceil_div(p.rows, rows)), rows * sh.threads, 0, s>>>(p);
+            return 0;
+        });
+    }
     return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
 }
 
+// The backward pass holds two sums a value in registers, so a thread takes 16 values at
+// most, and its rows go through shared memory.
+constexpr int64_t kRingBytes = 220 << 10;
+template <class IO, class R, int G>
+int64_t bwd_smem(int64_t D, int ve, bool dres, int rows) {
+    const int64_t weight = (D * 4 + 15) / 16 * 16, sums = G ? rows * D * 4 : 0;
+    const int64_t ring = ve > 1 ? rows * norm::bwd_stages<G>() * norm::bwd_row_bytes<IO, R>(D, dres) : 0;
+    return weight + (ring > sums ? ring : sums);
+}
 template <class IO, class R>
-int launch_backward(const norm::BwdParams &p, bool rms, float *dweight, float *dbias, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(bwd_blocks(p.rows));
-    if (rms)
-        norm::norm_backward_kernel<IO, R, true><<<grid, norm::kRowThreads, 0, s>>>(p);
-    else
-        norm::norm_backward_kernel<IO, R, false><<<grid, norm::kRowThreads, 0, s>>>(p);
+RowShape bwd_row_shape(int64_t D, bool dres) {
+    RowShape sh = row_shape(D, sizeof(IO));
+    const int64_t n = D / sh.ve, smem = bwd_smem<IO, R, 0>(D, sh.ve, dres, 1);
+    if (sh.ve == 1) {
+        if (n > 8 * norm::kBwdThreads) sh.nv = 0;
+        return sh;
+    }
+    const int most = 16 / sh.ve;  // vectors a thread
+    if (smem > kRingBytes || n > int64_t(most) * norm::kBwdThreads) return {sh.ve, 0, 0};
+    if (sh.threads <= 32 && sh.nv <= most) return sh;
+    // as few values a thread as leaves the SM's threads to as many rows as its shared memory holds
+    const int64_t want = norm::kBwdThreads / (smem * 2 > kRingBytes ? 1 : smem * 4 > kRingBytes ? 2 : 4);
+    int nv = 1;
+    while (nv < most && n > want * nv) nv *= 2;
+    return {sh.ve, nv, static_cast<int>(ceil_div(n, 32 * nv) * 32)};
+}
+
+// Backward blocks, each leaving one row of partial sums per gradient.
+constexpr int64_t kMaxBwdBlocks = 148 * 4;
+constexpr int kBwdGroupThreads = 256;  // of a block of several rows
+
+template <class IO, class R>
+int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cudaStream_t s) {
+    const RowShape sh = bwd_row_shape<IO, R>(p.D, p.dresidual != nullptr);
+    const int block_rows = sh.nv != 0 && sh.threads <= 32 ? kBwdGroupThreads / sh.threads : 1;
+    int64_t blocks = ceil_div(p.rows, block_rows);
+    int rc = SSCAN_OK;
+    auto at_most = [&](int64_t n) { blocks = blocks < n ? blocks : n; };
+    if (sh.nv == 0) {
+        at_most(148 * 2);
+        norm::norm_backward_long_kernel<IO, R><<<static_cast<unsigned>(blocks), norm::kLongThreads, 0, s>>>(p);
+    } else {
+        rc = with_shape<sizeof(IO)>(sh, [&](auto ve, auto nv, auto g) -> int {
+            if constexpr (ve * nv > 16) {
+                return SSCAN_ERR_INVALID;  // not a shape of bwd_row_shape
+            } else {
+                constexpr auto kern = norm::norm_backward_kernel<IO, R, ve, nv, g>;
+                const int64_t smem = bwd_smem<IO, R, g>(p.D, ve, p.dresidual != nullptr, block_rows);
+                const int threads = g ? kBwdGroupThreads : sh.threads;
+                int per_sm = static_cast<int>((kRingBytes + 7 * 1024) / (smem + 1024));  // blocks of an SM
+                if (per_sm * threads > norm::kBwdThreads) per_sm = norm::kBwdThreads / threads;
+                at_most(148 * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm));
+                if (smem_opt_in<kern>(static_cast<int>(kRingBytes)) != cudaSuccess) return SSCAN_ERR_CUDA;
+                kern<<<static_cast<unsigned>(blocks), threads, smem, s>>>(p);
+                return SSCAN_OK;
+            }
+        });
+    }
+    if (rc != SSCAN_OK) return rc;
     if (cudaGetLastError() != cudaSuccess) return SSCAN_ERR_CUDA;
     if (!dweight && !dbias) return SSCAN_OK;
-    const ColumnSums cs = {p.part, {dweight, dbias}, grid, p.D, int64_t(grid) * p.D};
+    const ColumnSums cs = {p.part, {dweight, dbias}, blocks, p.D, blocks * p.D};
     column_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(p.D, 32)), 2), kColThreads, 0, s>>>(cs);
     return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
 }
@@ -75,16 +170,16 @@ int sscan_norm_forward(int64_t rows, int64_t D, int dtype, uint32_t flags, float
     if (bc != SSCAN_OK) return bc;
     if (rows == 0) return SSCAN_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const norm::FwdParams p = {x, residual, weight, bias, y, residual_out, mean, rstd, rows, D, eps};
+    const norm::FwdParams p = {x, residual, weight, bias, y, residual_out, mean, rstd, rows, D, eps, rms};
     if (dtype == SSCAN_F32)
-        return residual ? launch_forward<float, float, true>(p, rms, s) : launch_forward<float, float, false>(p, rms, s);
-    if (!residual) return launch_forward<uint16_t, uint16_t, false>(p, rms, s);
-    return rf32 ? launch_forward<uint16_t, float, true>(p, rms, s) : launch_forward<uint16_t, uint16_t, true>(p, rms, s);
+        return residual ? launch_forward<float, float, true>(p, s) : launch_forward<float, float, false>(p, s);
+    if (!residual) return launch_forward<uint16_t, uint16_t, false>(p, s);
+    return rf32 ? launch_forward<uint16_t, float, true>(p, s) : launch_forward<uint16_t, uint16_t, true>(p, s);
 }
 
 size_t sscan_norm_backward_workspace_bytes(int64_t rows, int64_t D) {
     if (check_sizes(rows, D, SSCAN_F32, 0) != SSCAN_OK || rows == 0) return 0;
-    return round_up_256(2 * size_t(bwd_blocks(rows)) * size_t(D) * sizeof(float));
+    return round_up_256(2 * size_t(rows < kMaxBwdBlocks ? rows : kMaxBwdBlocks) * size_t(D) * sizeof(float));
 }
 
 int sscan_norm_backward(int64_t rows, int64_t D, int dtype, uint32_t flags, const void *dy, const void *s_in,
@@ -114,10 +209,10 @@ int sscan_norm_backward(int64_t rows, int64_t D, int dtype, uint32_t flags, cons
         return SSCAN_OK;
     }
     const norm::BwdParams p = {dy, s_in, dresidual, mean, rstd, weight, ds, dx, static_cast<float *>(workspace),
-                               rows, D, dweight != nullptr, dbias != nullptr};
-    if (dtype == SSCAN_F32) return launch_backward<float, float>(p, rms, dweight, dbias, s);
-    return rf32 ? launch_backward<uint16_t, float>(p, rms, dweight, dbias, s)
-                : launch_backward<uint16_t, uint16_t>(p, rms, dweight, dbias, s);
+                               rows, D, rms, dweight != nullptr, dbias != nullptr};
+    if (dtype == SSCAN_F32) return launch_backward<float, float>(p, dweight, dbias, s);
+    return rf32 ? launch_backward<uint16_t, float>(p, dweight, dbias, s)
+                : launch_backward<uint16_t, uint16_t>(p, dweight, dbias, s);
 }
 
 }  // extern "C"

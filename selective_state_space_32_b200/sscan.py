@@ -7,6 +7,7 @@ no fallback: if the library is missing or the call fails, this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -366,53 +367,59 @@ def ssd_forward(x, delta, A, B, C, h0=None, y=None, h_final=None, want_final: bo
 
 
 # --------------------------------------------------------------------------
-# Recurrent block operators: the gated linear recurrence and the layer norm.
+# Recurrent block operators: the gated linear recurrence and the layer norm.  A decode
+# step runs in a few microseconds on the device, so these wrappers keep to what a call
+# needs: checks of attributes, one allocation per output, the current stream's handle.
+
+_F32 = torch.float32
+
 
 def _want(name, t, shape, dt, dev):
-    """Raise unless t is a contiguous CUDA tensor of this shape, dtype and device."""
-    if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_cuda or not t.is_contiguous():
+    """Raise unless t is a contiguous tensor of this shape, dtype and (CUDA) device."""
+    if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: want contiguous CUDA {dt} {tuple(shape)} on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
 
-class _On:
-    """Context of one call: the tensors' device current, and new tensors allocated on the
-    call's stream (so that the allocator knows who uses them).  Entered only when either
-    differs from what is current."""
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-
-    def __enter__(self):
-        self._d = torch.cuda.device(self.dev)
-        self._d.__enter__()
-        self._s = torch.cuda.stream(self.stream)
-        self._s.__enter__()
-
-    def __exit__(self, *exc):
-        self._s.__exit__(*exc)
-        self._d.__exit__(*exc)
-
-
-def _on_device(fn, ref, stream, kw):
-    """Run fn(stream pointer, **kw) with ref's device current on ``stream`` (default: that
-    device's current stream)."""
+def _run(fn, ref, stream, args):
+    """fn(stream handle, *args) with ref's device current and new tensors allocated on the
+    call's stream, so that the allocator knows who uses them (stream None: the current
+    stream of ref's device)."""
     if not ref.is_cuda:
         raise ValueError(f"want CUDA tensors, got one on {ref.device}")
     dev = ref.device
     if stream is None:
-        cur = torch.cuda.current_stream(dev)
         if torch.cuda.current_device() == dev.index:
-            return fn(cur.cuda_stream, **kw)
-        stream = cur
+            return fn(torch._C._cuda_getCurrentRawStream(dev.index), *args)
+        stream = torch.cuda.current_stream(dev)
     elif stream.device != dev:
         raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-    with _On(dev, stream):
-        return fn(stream.cuda_stream, **kw)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return fn(stream.cuda_stream, *args)
 
 
 def _adr(t):
     return None if t is None else t.data_ptr()
+
+
+def _workspace(given, nbytes, like):
+    if given is None:
+        return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    if given.dtype != torch.uint8 or given.device != like.device or not given.is_contiguous() or given.numel() < nbytes:
+        raise ValueError(f"workspace: want at least {nbytes} contiguous uint8 on {like.device}, got {given.dtype} "
+                         f"{tuple(given.shape)} on {given.device}")
+    return given
+
+
+@functools.lru_cache(maxsize=1024)
+def _glr_sizes(B: int, L: int, D: int):
+    """(values of the saved states, bytes of the backward pass's workspace) of a shape"""
+    return (int(lib().sscan_glr_states_bytes(B, L, D)) // 4, int(lib().sscan_glr_backward_workspace_bytes(B, L, D)))
+
+
+def new_glr_states(B: int, L: int, D: int, device="cuda") -> torch.Tensor:
+    """A buffer for the states that ``glr_forward`` saves for ``glr_backward``."""
+    return torch.empty(_glr_sizes(B, L, D)[0], dtype=_F32, device=device)
 
 
 def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=None, want_final: bool = True,
@@ -425,14 +432,7 @@ def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=No
     of ``new_glr_states`` as ``states``).  Work and new tensors are on ``stream`` (default:
     the current stream of x's device).
     Returns (y [B, L, D], h_final [B, D] float32 or None, states or None)."""
-    return _on_device(_glr_forward, x, stream, dict(
-        x=x, gate=gate, rate=rate, input_gate=input_gate, h0=h0, y=y, h_final=h_final, want_final=want_final,
-        states=states, want_states=want_states))
-
-
-def new_glr_states(B: int, L: int, D: int, device="cuda") -> torch.Tensor:
-    """A buffer for the states that ``glr_forward`` saves for ``glr_backward``."""
-    return torch.empty(int(lib().sscan_glr_states_bytes(B, L, D)) // 4, dtype=torch.float32, device=device)
+    return _run(_glr_forward, x, stream, (x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states))
 
 
 def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states):
@@ -446,21 +446,21 @@ def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, stat
     if input_gate is not None:
         _want("input_gate", input_gate, shape, dt, dev)
     if rate is not None:
-        _want("rate", rate, (D,), torch.float32, dev)
+        _want("rate", rate, (D,), _F32, dev)
     if h0 is not None:
-        _want("h0", h0, (B, D), torch.float32, dev)
+        _want("h0", h0, (B, D), _F32, dev)
     if y is None:
         y = torch.empty_like(x)
     else:
         _want("y", y, shape, dt, dev)
     if h_final is not None:
-        _want("h_final", h_final, (B, D), torch.float32, dev)
+        _want("h_final", h_final, (B, D), _F32, dev)
     elif want_final:
-        h_final = torch.empty((B, D), dtype=torch.float32, device=dev)
+        h_final = x.new_empty((B, D), dtype=_F32) if h0 is None else torch.empty_like(h0)
     if states is not None:
-        _want("states", states, (int(lib().sscan_glr_states_bytes(B, L, D)) // 4,), torch.float32, dev)
+        _want("states", states, (_glr_sizes(B, L, D)[0],), _F32, dev)
     elif want_states:
-        states = new_glr_states(B, L, D, dev)
+        states = x.new_empty(_glr_sizes(B, L, D)[0], dtype=_F32)
     rc = lib().sscan_glr_forward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0),
                                  y.data_ptr(), _adr(h_final), _adr(states), st)
     if rc != OK:
@@ -476,18 +476,7 @@ def glr_backward(x, gate, dy, states, rate=None, input_gate=None, dh_final=None,
     without an input gate), drate ([D] float32, None without a rate) and dh0 ([B, D]
     float32, None unless wanted).  ``workspace``: a CUDA uint8 tensor of at least
     ``sscan_glr_backward_workspace_bytes`` (default: allocated here)."""
-    return _on_device(_glr_backward, x, stream, dict(
-        x=x, gate=gate, dy=dy, states=states, rate=rate, input_gate=input_gate, dh_final=dh_final, want_dh0=want_dh0,
-        workspace=workspace))
-
-
-def _workspace(given, nbytes, dev):
-    if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous() or given.numel() < nbytes:
-        raise ValueError(f"workspace: want at least {nbytes} contiguous uint8 on {dev}, got {given.dtype} "
-                         f"{tuple(given.shape)} on {given.device}")
-    return given
+    return _run(_glr_backward, x, stream, (x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace))
 
 
 def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace):
@@ -499,21 +488,23 @@ def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0,
     _want("x", x, shape, dt, dev)
     _want("gate", gate, shape, dt, dev)
     _want("dy", dy, shape, dt, dev)
-    _want("states", states, (int(lib().sscan_glr_states_bytes(B, L, D)) // 4,), torch.float32, dev)
+    n_states, n_workspace = _glr_sizes(B, L, D)
+    _want("states", states, (n_states,), _F32, dev)
+    dig = drate = dh0 = None
     if input_gate is not None:
         _want("input_gate", input_gate, shape, dt, dev)
+        dig = torch.empty_like(x)
     if dh_final is not None:
-        _want("dh_final", dh_final, (B, D), torch.float32, dev)
-    dx, dgate = torch.empty_like(x), torch.empty_like(x)
-    dig = torch.empty_like(x) if input_gate is not None else None
-    dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) if want_dh0 else None
-    drate = None
+        _want("dh_final", dh_final, (B, D), _F32, dev)
+    if want_dh0:
+        dh0 = x.new_empty((B, D), dtype=_F32) if dh_final is None else torch.empty_like(dh_final)
     if rate is not None:
-        _want("rate", rate, (D,), torch.float32, dev)
+        _want("rate", rate, (D,), _F32, dev)
         drate = torch.empty_like(rate)
-        workspace = _workspace(workspace, int(lib().sscan_glr_backward_workspace_bytes(B, L, D)), dev)
+        workspace = _workspace(workspace, n_workspace, x)
     else:
         workspace = None
+    dx, dgate = torch.empty_like(x), torch.empty_like(x)
     rc = lib().sscan_glr_backward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate),
                                   states.data_ptr(), dy.data_ptr(), _adr(dh_final), dx.data_ptr(), dgate.data_ptr(),
                                   _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
@@ -527,7 +518,7 @@ def _norm_types(x_dt, r_dt):
     code = _dtype_code(x_dt)
     if r_dt == x_dt:
         return code, 0
-    if r_dt == torch.float32:
+    if r_dt == _F32:
         return code, NORM_RESIDUAL_F32
     raise TypeError(f"residual of {r_dt} with x of {x_dt} (the same, or float32)")
 
@@ -543,8 +534,7 @@ def norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5, rm
     mean and rstd float32, one per row (mean None with rms, both None unless
     ``want_stats``).  Work and new tensors are on ``stream`` (default: the current stream
     of x's device)."""
-    return _on_device(_norm_forward, x, stream, dict(x=x, weight=weight, bias=bias, residual=residual, eps=eps, rms=rms,
-                                                     want_stats=want_stats))
+    return _run(_norm_forward, x, stream, (x, weight, bias, residual, eps, rms, want_stats))
 
 
 def _norm_forward(st, x, weight, bias, residual, eps, rms, want_stats):
@@ -552,28 +542,33 @@ def _norm_forward(st, x, weight, bias, residual, eps, rms, want_stats):
     if len(shape) < 1:
         raise ValueError("x: want [..., D]")
     D = shape[-1]
-    code, flags = _norm_types(dt, dt if residual is None else residual.dtype)
     _want("x", x, shape, dt, dev)
-    s = x
-    if residual is not None:
+    if residual is None:
+        code, flags, s = _dtype_code(dt), 0, x
+    else:
+        code, flags = _norm_types(dt, residual.dtype)
         _want("residual", residual, shape, residual.dtype, dev)
         s = torch.empty_like(residual)
     if weight is not None:
-        _want("weight", weight, (D,), torch.float32, dev)
+        _want("weight", weight, (D,), _F32, dev)
     if bias is not None:
-        _want("bias", bias, (D,), torch.float32, dev)
-    rows = shape[:-1].numel()
+        _want("bias", bias, (D,), _F32, dev)
     y = torch.empty_like(x)
     mean = rstd = None
     if want_stats:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        rstd = x.new_empty(shape[:-1], dtype=_F32)
         mean = None if rms else torch.empty_like(rstd)
-    rc = lib().sscan_norm_forward(rows, D, code, flags | (NORM_RMS if rms else 0), eps, x.data_ptr(), _adr(residual),
-                                  _adr(weight), _adr(bias), y.data_ptr(), None if residual is None else s.data_ptr(),
-                                  _adr(mean), _adr(rstd), st)
+    rc = lib().sscan_norm_forward(shape[:-1].numel(), D, code, flags | (NORM_RMS if rms else 0), eps, x.data_ptr(),
+                                  _adr(residual), _adr(weight), _adr(bias), y.data_ptr(),
+                                  None if residual is None else s.data_ptr(), _adr(mean), _adr(rstd), st)
     if rc != OK:
         raise SscanError(rc, "sscan_norm_forward")
     return y, s, mean, rstd
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows: int, D: int) -> int:
+    return int(lib().sscan_norm_backward_workspace_bytes(rows, D))
 
 
 def norm_backward(dy, s, mean, rstd, weight=None, dresidual=None, rms: bool = False, want_dweight: bool = True,
@@ -584,37 +579,38 @@ def norm_backward(dy, s, mean, rstd, weight=None, dresidual=None, rms: bool = Fa
     dx (dtype of dy), dresidual (dtype of s; the same tensor as dx where the types are
     equal), dweight and dbias ([D] float32 or None).  ``workspace``: a CUDA uint8 tensor of
     at least ``sscan_norm_backward_workspace_bytes`` (default: allocated here)."""
-    return _on_device(_norm_backward, dy, stream, dict(
-        dy=dy, s=s, mean=mean, rstd=rstd, weight=weight, dresidual=dresidual, rms=rms, want_dweight=want_dweight,
-        want_dbias=want_dbias, workspace=workspace))
+    return _run(_norm_backward, dy, stream, (dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace))
 
 
 def _norm_backward(st, dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace):
     shape, dt, dev = dy.shape, dy.dtype, dy.device
     if len(shape) < 1:
         raise ValueError("dy: want [..., D]")
-    D = shape[-1]
+    D, row_shape = shape[-1], shape[:-1]
     code, flags = _norm_types(dt, s.dtype)
     _want("dy", dy, shape, dt, dev)
     _want("s", s, shape, s.dtype, dev)
-    _want("rstd", rstd, shape[:-1], torch.float32, dev)
+    _want("rstd", rstd, row_shape, _F32, dev)
     if not rms:
         if mean is None:
             raise ValueError("mean: wanted without rms")
-        _want("mean", mean, shape[:-1], torch.float32, dev)
+        _want("mean", mean, row_shape, _F32, dev)
     elif mean is not None:
         raise ValueError("mean: must be None with rms")
+    dweight = dbias = None
     if weight is not None:
-        _want("weight", weight, (D,), torch.float32, dev)
+        _want("weight", weight, (D,), _F32, dev)
+        if want_dweight:
+            dweight = torch.empty_like(weight)
     if dresidual is not None:
         _want("dresidual", dresidual, shape, s.dtype, dev)
-    rows = shape[:-1].numel()
+    rows = row_shape.numel()
     ds = torch.empty_like(s)
     dx = torch.empty_like(dy) if s.dtype != dt else None
-    dweight = torch.empty_like(weight) if weight is not None and want_dweight else None
-    dbias = torch.empty((D,), dtype=torch.float32, device=dev) if want_dbias else None
+    if want_dbias:
+        dbias = dy.new_empty((D,), dtype=_F32) if weight is None else torch.empty_like(weight)
     if dweight is not None or dbias is not None:
-        workspace = _workspace(workspace, int(lib().sscan_norm_backward_workspace_bytes(rows, D)), dev)
+        workspace = _workspace(workspace, _norm_workspace(rows, D), dy)
     else:
         workspace = None
     rc = lib().sscan_norm_backward(rows, D, code, flags | (NORM_RMS if rms else 0), dy.data_ptr(), s.data_ptr(),

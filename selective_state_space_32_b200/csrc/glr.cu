@@ -37,29 +37,33 @@ struct Shape {
     int warps, cluster;
 };
 
-// `chains` = batch rows times channel groups, `n` = runs of the sequence.  Measured on B200
-// (us; warps x blocks): about ten warps an SM are wanted, in small blocks first: 192 chains
-// of 2048 tokens, bf16 with rate and input gate: 4x2 54, 4x1 74, 8x4 58; 384 fp32 chains:
-// 4x1 49, 8x1 56, 4x2 56; 128 chains of 8192 tokens: 4x4 81, 4x2 95, 8x8 105.  Where that
-// leaves the device half empty, blocks of 8 warps (32 chains of 131072 tokens: 8x8 621, 4x8
-// 632, backward 1135 against 1422), and for a handful of chains clusters of 16 (1 chain of
-// 65536 tokens: 8x16 95, 8x8 205).  With very many chains fewer warps share one: 2048 chains
-// of 32 tokens, backward: 2x1 19.7, 4x1 21.0.
-Shape scan_shape(int64_t chains, int64_t n) {
-    constexpr int64_t kWant = 148 * 10;
+// `chains` = batch rows times channel groups, `n` = runs of the sequence, `want` = warps that
+// fill the device.  Measured on B200 (us; warps x blocks): about ten warps an SM are wanted,
+// in small blocks first: 192 chains of 2048 tokens, bf16 with rate and input gate: 4x2 54,
+// 4x1 74, 8x4 58; 384 fp32 chains: 4x1 49, 8x1 56, 4x2 56; 128 chains of 8192 tokens: 4x4 81,
+// 4x2 95, 8x8 105.  With enough chains, blocks of 8 warps instead of clusters of two (384
+// fp32 chains, backward: 8x1 89, 4x2 98).  Where that leaves the device half empty, 8 warps
+// as well (32 chains of 131072 tokens: 8x8 621, 4x8 632, backward 1135 against 1422), and for
+// a handful of chains clusters of 16 (1 chain of 65536 tokens: 8x16 95, 8x8 205).  With very
+// many chains fewer warps share one.
+Shape scan_shape(int64_t chains, int64_t n, int64_t want) {
     int w = 1;
     while (w < 4 && w < n) w *= 2;
-    while (w > 1 && chains * w >= 8192) w /= 2;
+    while (w > 1 && chains * w >= 16384) w /= 2;
     auto cluster = [&](int most) {
         int c = 1;
-        while (c < most && c * w < n && chains * w * c < kWant) c *= 2;
+        while (c < most && c * w < n && chains * w * c < want) c *= 2;
         return c;
     };
     int c = cluster(8);
-    if (w * c < n && chains * w * c < kWant) w = glr::kMaxWarps, c = cluster(8);
-    if (w * c < n && chains * w * c < kWant / 4) c = cluster(glr::kMaxCluster);
+    if (w == 4 && c == 2 && chains >= 2 * 148) w = glr::kMaxWarps, c = 1;
+    if (w * c < n && chains * w * c < want) w = glr::kMaxWarps, c = cluster(8);
+    if (w * c < n && chains * w * c < want / 4) c = cluster(glr::kMaxCluster);
     return {w, c};
 }
+constexpr int64_t kForwardWarps = 148 * 10;
+// the backward pass's, by the blocks that an SM holds
+constexpr int64_t backward_warps(int blocks) { return 148 * (blocks == 3 ? 13 : 10); }
 
 template <class IO>
 bool staged(int64_t D) { return D * int64_t(sizeof(IO)) % 16 == 0; }
@@ -108,7 +112,7 @@ int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
     }
     constexpr int K = glr::kForwardRun;
     const int64_t groups = ceil_div(p.D, ch);
-    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K));
+    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), kForwardWarps);
     constexpr auto kern = glr::glr_scan_kernel<IO, STAGED, DECAY, IG, K>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
@@ -127,7 +131,7 @@ template <class IO, bool STAGED, bool DECAY, bool IG>
 int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
     constexpr int NS = IG ? 4 : 3, ch = 32 * glr::lane_channels<IO, STAGED>();
     const int64_t groups = ceil_div(p.D, ch);
-    const Shape sh = scan_shape(p.B * groups, p.nruns);
+    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(glr::scan_blocks<IO, STAGED>()));
     constexpr auto kern = glr::glr_scan_backward_kernel<IO, STAGED, DECAY, IG>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(glr::kMaxWarps, glr::kMaxCluster)) !=
         cudaSuccess)

@@ -36,6 +36,10 @@ constexpr int kForwardRun = 16;  // tokens of a warp's run; the backward pass ta
 
 // channels a lane holds
 template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
+// Blocks of kMaxWarps an SM holds.  One channel a lane: 80 registers, three (384 fp32 chains
+// of 2048 tokens, backward: 89 us, with two blocks 106); two: 128, since 80 would spill (bf16
+// with rate and input gate, 192 chains, backward: two blocks 103 us, three 113).
+template <class IO, bool STAGED> constexpr int scan_blocks() { return lane_channels<IO, STAGED>() == 1 ? 3 : 2; }
 
 template <class IO, bool STAGED, int NS, int K>
 constexpr int scan_smem_bytes(int warps, int cluster) {
@@ -316,7 +320,8 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
 
 // grid: B * groups * C blocks of 32 W threads in clusters of C
 template <class IO, bool STAGED, bool DECAY, bool IG, int K>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
+__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<IO, STAGED>())
+glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 3 : 2;
     using Loader = RunLoader<IO, STAGED, NS, K>;
     constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
@@ -403,7 +408,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_kernel(const FwdPa
 // The walk from the last token.  part (with a rate): row b * C + rank holds the sums of
 // this block's channels.
 template <class IO, bool STAGED, bool DECAY, bool IG>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
+__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<IO, STAGED>())
+glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 4 : 3, K = kRun;
     using Loader = RunLoader<IO, STAGED, NS, K>;
     constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;

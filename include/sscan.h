@@ -285,21 +285,24 @@ SSCAN_API int sscan_ssd_forward(int64_t B, int64_t L, int64_t H, int64_t P, int6
  *   dtype              SSCAN_F32 or SSCAN_BF16: x, the gates and y
  *   x, gate            [B][L][D]
  *   input_gate         [B][L][D], or NULL
- *   rate               [D] fp32, every value > 0, or NULL.  (A rate of 0 holds the state;
- *                      its gradient is not defined.)
+ *   rate               [D] fp32, every value > 0, or NULL.  Values above 80 (a decay of
+ *                      2e-35 at s = 1) act as 80.  (A rate of 0 holds the state; its
+ *                      gradient is not defined.)
  *   h0                 [B][D] fp32, or NULL for a zero initial state
  *   y                  [B][L][D] (output)
  *   h_final            [B][D] fp32 (output), or NULL; may be the same buffer as h0
  *   states             sscan_glr_states_bytes(B, L, D) bytes (output), or NULL: states
  *                      along the sequence that sscan_glr_backward continues from.  Their
  *                      layout is the library's own.
- * Gates of +-infinity mean exactly 1 and 0.  A state that is infinite or NaN makes the
- * later outputs of its channel and batch row infinite or NaN, and no others.
+ * Gates of +-infinity are 1 and 0 to within 2^-126.  A state that is infinite or NaN makes
+ * the later outputs of its channel and batch row infinite or NaN, and no others.
  * The state and all arithmetic are fp32; sums run in an order that the sizes fix, so equal
  * calls give equal bits.  Keeps nothing between calls: it may be captured in a CUDA graph.
  * Every pointer is caller-owned device memory, 16-byte aligned; outputs must not overlap
  * inputs (but h_final = h0) nor each other.  Asynchronous on `stream`.  Errors as for
- * sscan_forward. */
+ * sscan_forward; B D >= 2^31, D > 2^28 and B L D > 2^48 are SSCAN_ERR_UNSUPPORTED.  The
+ * blocks that share a sequence wait for one another inside a kernel for a bounded time;
+ * should such a wait give up, the values that depend on it are NaN. */
 SSCAN_API size_t sscan_glr_states_bytes(int64_t B, int64_t L, int64_t D);
 SSCAN_API int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
                                 const void *input_gate, const float *rate, const float *h0, void *y,
@@ -350,7 +353,8 @@ enum {
  * Sums are fp32 in an order that the sizes fix (variance from centred squares).  No
  * workspace; nothing is kept between calls, so it may be captured in a CUDA graph.  Every
  * pointer is caller-owned device memory, 16-byte aligned; outputs must not overlap inputs
- * nor each other.  Asynchronous on `stream`.  Errors as for sscan_forward. */
+ * nor each other.  Asynchronous on `stream`.  Errors as for sscan_forward; rows >= 2^31 and
+ * D > 2^28 are SSCAN_ERR_UNSUPPORTED. */
 SSCAN_API int sscan_norm_forward(int64_t rows, int64_t D, int dtype, uint32_t flags, float eps, const void *x,
                                  const void *residual, const float *weight, const float *bias, void *y,
                                  void *residual_out, float *mean, float *rstd, void *stream);

@@ -101,43 +101,43 @@ struct Launch {
     }
 };
 
-template <class IO, bool STAGED, bool DECAY, bool IG>
+template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
-    constexpr int NS = IG ? 3 : 2, ch = 32 * glr::lane_channels<IO, STAGED>();
-    if (p.L <= kStepTokens) {
-        constexpr int V = STAGED ? 2 : 1;
-        const int64_t blocks = ceil_div(p.B * p.D, V * glr::kStepThreads);
-        glr::glr_step_kernel<IO, V, DECAY, IG><<<static_cast<unsigned>(blocks), glr::kStepThreads, 0, s>>>(p);
-        return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
-    }
-    constexpr int K = glr::kForwardRun;
-    const int64_t groups = ceil_div(p.D, ch);
+    constexpr int NS = IG ? 3 : 2, K = glr::kForwardRun;
+    const int64_t groups = ceil_div(p.D, 32 * V);
     const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), kForwardWarps);
-    constexpr auto kern = glr::glr_scan_kernel<IO, STAGED, DECAY, IG, K>;
-    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
+    constexpr auto kern = glr::glr_scan_kernel<IO, V, STAGED, DECAY, IG, K>;
+    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
-    const int64_t blocks = p.B * groups * sh.cluster;
-    Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, K>(sh.warps, sh.cluster), s);
+    Launch l(p.B * groups * sh.cluster, sh, glr::scan_smem_bytes<IO, V, STAGED, NS, K>(sh.warps, sh.cluster), s);
     return cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) == cudaSuccess ? SSCAN_OK
                                                                                                        : SSCAN_ERR_CUDA;
 }
 
 template <class IO, bool DECAY, bool IG>
 int launch_forward(const glr::FwdParams &p, cudaStream_t s) {
-    return staged<IO>(p.D) ? launch_scan<IO, true, DECAY, IG>(p, s) : launch_scan<IO, false, DECAY, IG>(p, s);
+    if (p.L <= kStepTokens) {
+        const bool pairs = p.D % 2 == 0;
+        const unsigned blocks = static_cast<unsigned>(ceil_div(p.B * p.D, (pairs ? 2 : 1) * glr::kStepThreads));
+        if (pairs)
+            glr::glr_step_kernel<IO, 2, DECAY, IG><<<blocks, glr::kStepThreads, 0, s>>>(p);
+        else
+            glr::glr_step_kernel<IO, 1, DECAY, IG><<<blocks, glr::kStepThreads, 0, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
+    }
+    if (!staged<IO>(p.D)) return launch_scan<IO, 1, false, DECAY, IG>(p, s);
+    return launch_scan<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, s);
 }
 
-template <class IO, bool STAGED, bool DECAY, bool IG>
+template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
-    constexpr int NS = IG ? 4 : 3, ch = 32 * glr::lane_channels<IO, STAGED>();
-    const int64_t groups = ceil_div(p.D, ch);
-    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(glr::scan_blocks<IO, STAGED>()));
-    constexpr auto kern = glr::glr_scan_backward_kernel<IO, STAGED, DECAY, IG>;
-    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(glr::kMaxWarps, glr::kMaxCluster)) !=
-        cudaSuccess)
+    constexpr int NS = IG ? 4 : 3, K = glr::kRun;
+    const int64_t groups = ceil_div(p.D, 32 * V);
+    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(glr::scan_blocks<V>()));
+    constexpr auto kern = glr::glr_scan_backward_kernel<IO, V, STAGED, DECAY, IG>;
+    if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
-    const int64_t blocks = p.B * groups * sh.cluster;
-    Launch l(blocks, sh, glr::scan_smem_bytes<IO, STAGED, NS, glr::kRun>(sh.warps, sh.cluster), s);
+    Launch l(p.B * groups * sh.cluster, sh, glr::scan_smem_bytes<IO, V, STAGED, NS, K>(sh.warps, sh.cluster), s);
     if (cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) != cudaSuccess) return SSCAN_ERR_CUDA;
     if (!DECAY) return SSCAN_OK;
     const ColumnSums cs = {p.part, {drate, nullptr}, p.B * sh.cluster, p.D, 0};
@@ -147,8 +147,8 @@ int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) 
 
 template <class IO, bool DECAY, bool IG>
 int launch_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
-    return staged<IO>(p.D) ? launch_scan_backward<IO, true, DECAY, IG>(p, drate, s)
-                           : launch_scan_backward<IO, false, DECAY, IG>(p, drate, s);
+    if (!staged<IO>(p.D)) return launch_scan_backward<IO, 1, false, DECAY, IG>(p, drate, s);
+    return launch_scan_backward<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, drate, s);
 }
 
 template <class IO>

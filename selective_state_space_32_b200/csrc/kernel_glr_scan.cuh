@@ -28,23 +28,27 @@
 namespace sscan {
 namespace glr {
 
-constexpr int kRowBytes = 128;
 constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 16;  // above 8 is not portable between devices; this one has 16
 constexpr int kStages = 2;
 constexpr int kForwardRun = 16;  // tokens of a warp's run; the backward pass takes kRun (a saved state each)
 
-// channels a lane holds
+// Channels a lane holds: a pair where rows are staged in bf16, or one.  (One channel a lane in
+// bf16 too, 64 bytes a row, measured slower wherever there is work to fill the device: 192
+// chains of 2048 tokens 59 us against 53, 128 of 8192 109 against 78, 32 of 131072 745
+// against 621; faster for a single chain of 65536 only, 71 against 94.)
 template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
 // Blocks of kMaxWarps an SM holds.  One channel a lane: 80 registers, three (384 fp32 chains
 // of 2048 tokens, backward: 89 us, with two blocks 106); two: 128, since 80 would spill (bf16
 // with rate and input gate, 192 chains, backward: two blocks 103 us, three 113).
-template <class IO, bool STAGED> constexpr int scan_blocks() { return lane_channels<IO, STAGED>() == 1 ? 3 : 2; }
+template <int V> constexpr int scan_blocks() { return V == 1 ? 3 : 2; }
 
-template <class IO, bool STAGED, int NS, int K>
+// Bytes of a staged row: the channels of a warp
+template <class IO, int V> constexpr int row_bytes() { return 32 * V * Io<IO>::kBytes; }
+
+template <class IO, int V, bool STAGED, int NS, int K>
 constexpr int scan_smem_bytes(int warps, int cluster) {
-    const int ch = 32 * lane_channels<IO, STAGED>();
-    return 128 + (STAGED ? warps * kStages * NS * K * kRowBytes : 0) + 2 * (warps + cluster) * ch * 8;
+    return 128 + (STAGED ? warps * kStages * NS * K * row_bytes<IO, V>() : 0) + 2 * (warps + cluster) * 32 * V * 8;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -107,11 +111,11 @@ template <class IO> __device__ __forceinline__ void store_lane(IO *p, f2 v) { st
 
 // One warp's view of its streams: NS tensors [B][L][D] in runs of K tokens, and a lane's
 // V channels of them as pairs (V = 2: the channels of one token; V = 1: two tokens).
-template <class IO, bool STAGED, int NS, int K>
+template <class IO, int V, bool STAGED, int NS, int K>
 struct RunLoader {
-    static constexpr int V = lane_channels<IO, STAGED>();
     static constexpr int CH = 32 * V, NP = K * V / 2;
-    static constexpr int kStageBytes = NS * K * kRowBytes;
+    static constexpr int kRowBytes = row_bytes<IO, V>(), kStageBytes = NS * K * kRowBytes;
+    static constexpr int kRowLanes = kRowBytes / 16, kRows = 32 / kRowLanes;  // lanes that copy a row, rows at once
     const IO *src[NS];  // batch row's first token, first channel of the group
     unsigned char *ring;
     int64_t L, D;
@@ -121,25 +125,27 @@ struct RunLoader {
     __device__ __forceinline__ void issue(int64_t t0, int stage) const {
         if constexpr (STAGED) {
             if (t0 >= 0 && t0 < L) {
-                const int col = (lane & 7) * (16 / Io<IO>::kBytes), row = lane >> 3;
-                const uint32_t own = row * D + col;  // 3 D at most: D is below 2^28 where rows are staged
-                const int64_t next = 4 * D;
-                unsigned char *dst = ring + stage * kStageBytes + row * kRowBytes + (lane & 7) * 16;
+                const int at16 = lane % kRowLanes, col = at16 * (16 / Io<IO>::kBytes), row = lane / kRowLanes;
+                const uint32_t own = row * static_cast<uint32_t>(D) + col;  // under 8 rows of 2^28 channels
+                const int64_t next = kRows * D;
+                unsigned char *dst = ring + stage * kStageBytes + row * kRowBytes + at16 * 16;
                 if (live == CH && t0 + K <= L) {
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
                         const IO *p = src[s] + t0 * D;
 #pragma unroll
-                        for (int h = 0; h < K / 4; ++h, p += next) cp_async16(dst + (s * K + 4 * h) * kRowBytes, p + own);
+                        for (int h = 0; h < K / kRows; ++h, p += next)
+                            cp_async16(dst + (s * K + kRows * h) * kRowBytes, p + own);
                     }
                 } else {
                     const int n = col < live ? (L - t0 < K ? static_cast<int>(L - t0) : K) : 0;
 #pragma unroll
                     for (int s = 0; s < NS; ++s)
 #pragma unroll
-                        for (int h = 0; h < K / 4; ++h)
-                            cp_async16_or_zeros(dst + (s * K + 4 * h) * kRowBytes,
-                                                row + 4 * h < n ? src[s] + t0 * D + h * next + own : src[s], row + 4 * h < n);
+                        for (int h = 0; h < K / kRows; ++h)
+                            cp_async16_or_zeros(dst + (s * K + kRows * h) * kRowBytes,
+                                                row + kRows * h < n ? src[s] + t0 * D + h * next + own : src[s],
+                                                row + kRows * h < n);
                 }
             }
             cp_async_commit();
@@ -148,12 +154,13 @@ struct RunLoader {
     // stream s, pair i of the run at t0 with n tokens
     __device__ __forceinline__ f2 pair(int64_t t0, int n, int stage, int s, int i) const {
         if constexpr (STAGED) {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(ring + stage * kStageBytes + s * K * kRowBytes) + lane;
+            const unsigned char *at = ring + stage * kStageBytes + s * K * kRowBytes;
             if constexpr (V == 2) {
-                const uint32_t v = w[i * 32];
+                const uint32_t v = reinterpret_cast<const uint32_t *>(at)[i * 32 + lane];
                 return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
             } else {
-                return pack2(__uint_as_float(w[2 * i * 32]), __uint_as_float(w[(2 * i + 1) * 32]));
+                const IO *w = reinterpret_cast<const IO *>(at) + lane;
+                return pack2(Io<IO>::widen(w[2 * i * 32]), Io<IO>::widen(w[(2 * i + 1) * 32]));
             }
         } else {
             const IO *p = src[s] + (t0 + 2 * i) * D + lane;
@@ -270,6 +277,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
             return h;
         }
         T h = carry;
+#pragma unroll 2
         for (int q = 0; q < warps; ++q, at += CH) {
             T ma, mh;
             load_map(at, ma, mh);
@@ -281,6 +289,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
     // the runs of this block before this one; the warps that send go on to the whole block
     T Ab = LV::splat(1.0f), Hb = LV::splat(0.0f);
     int q = 0;
+#pragma unroll 2
     for (; q < w; ++q, at += CH) {
         T ma, mh;
         load_map(at, ma, mh);
@@ -292,6 +301,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
         if (warps == 1) {
             Ab = A, Hb = H;
         } else {
+#pragma unroll 2
             for (; q < warps; ++q, at += CH) {
                 T ma, mh;
                 load_map(at, ma, mh);
@@ -309,6 +319,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
     if (threadIdx.x == 0) mbar_expect_tx(sh.bar + par, sh.C * CH * 8);  // for the second next step
     at = sh.cl + par * sh.C * CH + sh.lane * V;
     T h = carry;
+#pragma unroll 2
     for (uint32_t r = 0; r < sh.C; ++r, at += CH) {
         T ma, mh;
         load_map(at, ma, mh);
@@ -319,12 +330,12 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
 }
 
 // grid: B * groups * C blocks of 32 W threads in clusters of C
-template <class IO, bool STAGED, bool DECAY, bool IG, int K>
-__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<IO, STAGED>())
+template <class IO, int V, bool STAGED, bool DECAY, bool IG, int K>
+__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<V>())
 glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 3 : 2;
-    using Loader = RunLoader<IO, STAGED, NS, K>;
-    constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
+    using Loader = RunLoader<IO, V, STAGED, NS, K>;
+    constexpr int CH = Loader::CH, NP = Loader::NP;
     using LV = Lane<V>;
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -407,12 +418,12 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
 
 // The walk from the last token.  part (with a rate): row b * C + rank holds the sums of
 // this block's channels.
-template <class IO, bool STAGED, bool DECAY, bool IG>
-__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<IO, STAGED>())
+template <class IO, int V, bool STAGED, bool DECAY, bool IG>
+__global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<V>())
 glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 4 : 3, K = kRun;
-    using Loader = RunLoader<IO, STAGED, NS, K>;
-    constexpr int V = Loader::V, CH = Loader::CH, NP = Loader::NP;
+    using Loader = RunLoader<IO, V, STAGED, NS, K>;
+    constexpr int CH = Loader::CH, NP = Loader::NP;
     using LV = Lane<V>;
     using T = typename LV::T;
     extern __shared__ __align__(128) unsigned char smem[];

@@ -103,6 +103,54 @@ def test_many_rows(B, L, D):
     check(B, L, D, "bf16", False, True, True)
 
 
+@pytest.mark.parametrize("B,L,D,dtype", [
+    (1, 40000, 64, "bf16"),      # one chain: clusters of 16 blocks of 8 warps
+    (1, 9000, 96, "f32"),        # three chains
+    (2, 3000, 1024, "bf16"),     # 32 chains: clusters of 8
+    (8, 600, 1536, "bf16"),      # 192 chains: clusters of 2
+    (3, 300, 4096, "f32"),       # 384 chains: one block each, of 4 warps or of 8
+    (70, 17, 8000, "f32"),       # 17500 chains: one warp each
+    (3, 1000, 515, "bf16"),      # rows that are not a multiple of 16 bytes
+])
+def test_every_spread_of_the_walk(B, L, D, dtype):
+    check(B, L, D, dtype, True, L % 2 == 0, True)
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 values: the end of the sequence against a call on the end alone, from the state before it
+    (fp32: y holds the states), both within 1e-5 relative, the repository's fp32 tolerance."""
+    B, L, D, tail = 1, 1_060_000, 2056, 3000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    x, gate, dy = new(B, L, D), new(B, L, D), new(B, L, D)
+    rate = torch.rand(D, device="cuda", generator=gen) * 0.5 + 0.01
+    y, hf, st = S.glr_forward(x, gate, rate, want_states=True)
+    g = S.glr_backward(x, gate, dy, st, rate)
+    cut = L - tail
+    part = [t[:, cut:].clone() for t in (x, gate, dy)]
+    y2, hf2, st2 = S.glr_forward(part[0], part[1], rate, h0=y[:, cut - 1].contiguous(), want_states=True)
+    g2 = S.glr_backward(part[0], part[1], part[2], st2, rate)
+    rel = lambda a, b: float((a.double() - b.double()).norm() / b.double().norm())
+    assert rel(y[:, cut:], y2) < 1e-5 and rel(hf, hf2) < 1e-5
+    assert rel(g["dx"][:, cut:], g2["dx"]) < 1e-5 and rel(g["dgate"][:, cut:], g2["dgate"]) < 1e-5
+    # the first tokens' outputs do not depend on what follows
+    assert rel(y[:, :tail], S.glr_forward(x[:, :tail].clone(), gate[:, :tail].clone(), rate)[0]) < 1e-5
+
+
+def test_rates_above_80_act_as_80():
+    d = cuda(make(2, 300, 72, "f32", True, True, True))
+    d["rate"][::3] = 80.0
+    args = lambda r: (d["x"], d["gate"], r, d["input_gate"], d["h0"])
+    more = d["rate"].clone()
+    more[::3] = torch.tensor([1e3, float("inf"), 81.0, 1e30] * 6, device="cuda")
+    y, hf, st = S.glr_forward(*args(d["rate"]), want_states=True)
+    y2, hf2, st2 = S.glr_forward(*args(more), want_states=True)
+    assert torch.equal(y, y2) and torch.equal(hf, hf2) and torch.isfinite(y).all()
+    a = S.glr_backward(d["x"], d["gate"], d["dy"], st, d["rate"], d["input_gate"])
+    b = S.glr_backward(d["x"], d["gate"], d["dy"], st2, more, d["input_gate"])
+    assert all(torch.equal(a[k], b[k]) and torch.isfinite(a[k]).all() for k in a)
+
+
 def test_empty_sequence():
     d = cuda(make(2, 0, 24, "bf16", True, True, True))
     y, hf, st = S.glr_forward(d["x"], d["gate"], d["rate"], d["input_gate"], d["h0"], want_states=True)

@@ -23,18 +23,17 @@ static __global__ void __launch_bounds__(kColThreads) column_sums_kernel(const C
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     const float *part = p.part + blockIdx.y * p.plane_stride;
-    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    float a[8];  // eight loads in flight a thread: the kernel is a few rounds of latency
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = 0.0f;
     if (d < p.D) {
-        int64_t r = w;
-        for (; r + 96 < p.rows; r += 128) {
-            s0 += part[r * p.D + d];
-            s1 += part[(r + 32) * p.D + d];
-            s2 += part[(r + 64) * p.D + d];
-            s3 += part[(r + 96) * p.D + d];
+        for (int64_t r = w; r < p.rows; r += 256) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (r + 32 * k < p.rows) a[k] += part[(r + 32 * k) * p.D + d];
         }
-        for (; r < p.rows; r += 32) s0 += part[r * p.D + d];
     }
-    sm[w][lane] = (s0 + s1) + (s2 + s3);
+    sm[w][lane] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
     __syncthreads();
     // warp w joins the 32 sums of channel w of the block's 32, by a tree
     float s = sm[lane][w];

@@ -223,8 +223,9 @@ __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows of a ring, a group's or a block's
-template <int G> constexpr int bwd_stages() { return G ? 4 : 2; }
+// Rows of a ring: a group's, a block's, and a block's whose rows are so long that shared
+// memory holds only one (4000 rows of 8192 fp32 values with a residual)
+constexpr int kGroupStages = 4, kBlockStages = 2, kLongStages = 1;
 // Threads of an SM: a thread's sums and its values of the row take about 100 registers
 constexpr int kBwdThreads = 640;
 
@@ -234,20 +235,23 @@ __host__ __device__ constexpr int64_t bwd_row_bytes(int64_t D, bool dres) {
     return D * (Io<IO>::kBytes + (dres ? 2 : 1) * Io<R>::kBytes);
 }
 
-// A thread's NV VE values of a row as pairs (past the row's end: zeros), from memory or, with
-// `staged`, from shared memory.
+// The pair with the halves that are off replaced by 0
+__device__ __forceinline__ f2 and2(f2 v, bool lo, bool hi) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(lo ? a : 0.0f, hi ? b : 0.0f);
+}
+
+// A thread's NV VE values of a row as pairs, vector i at `at[i]` (in values), from memory or,
+// with `staged`, from shared memory.
 template <class X, int VE, int NV>
-__device__ __forceinline__ void load_pairs(const X *row, const unsigned char *staged, int t, int T, int nvec,
+__device__ __forceinline__ void load_pairs(const X *row, const unsigned char *staged, const int (&at)[NV],
                                            f2 (&v)[NV * VE / 2]) {
     Raw<X, VE> q[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int j = t + i * T;
-        q[i].zero();
-        if (j < nvec) {
-            if (staged != nullptr) q[i].load_shared(staged + j * VE * Io<X>::kBytes);
-            else q[i].load(row + j * VE);
-        }
+        if (staged != nullptr) q[i].load_shared(staged + at[i] * Io<X>::kBytes);
+        else q[i].load(row + at[i]);
     }
 #pragma unroll
     for (int k = 0; k < NV * VE / 2; ++k)
@@ -261,10 +265,10 @@ __device__ __forceinline__ void load_pairs(const X *row, const unsigned char *st
 // NV VE values are packed pairs: the pass would be bound by instructions otherwise.
 // Dynamic shared memory: the weight (D floats; ones without a weight), then the rings, used
 // again for the warps' sums (D floats each) at the end.
-template <class IO, class R, int VE, int NV, int G>
+template <class IO, class R, int VE, int NV, int G, int kStages>
 __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(const BwdParams p) {
     constexpr bool STAGED = VE > 1;
-    constexpr int kStages = bwd_stages<G>(), NP = NV * VE / 2;
+    constexpr int NP = NV * VE / 2;
     __shared__ float2 part[2][32];
     extern __shared__ __align__(16) unsigned char smem[];
     float *weight = reinterpret_cast<float *>(smem);
@@ -274,6 +278,16 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
     const int T = G ? G : blockDim.x, t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
     const int groups = G ? blockDim.x / (G ? G : 1) : 1, group = G ? threadIdx.x / (G ? G : 1) : 0;
     const int nvec = static_cast<int>(p.D / VE);
+    // this thread's vectors; in place of one past the row's end its first is read again (with
+    // a weight of 0) and nothing is written; a thread without any only joins the sums
+    int at[NV];
+    bool live[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int j = t + i * T;
+        live[i] = j < nvec;
+        at[i] = (live[i] ? j : t) * VE;
+    }
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     // a warp's groups walk together (their sums are exchanged in one instruction): they end
     // when the warp's first row is past the last, and a row past it is empty
@@ -283,23 +297,25 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
     const int64_t row_bytes = bwd_row_bytes<IO, R>(p.D, p.dresidual != nullptr);
     unsigned char *mine = ring + group * kStages * row_bytes;
     const int64_t off_s = p.D * Io<IO>::kBytes, off_d = off_s + p.D * Io<R>::kBytes;
+    const bool dres = p.dresidual != nullptr;
     auto issue = [&](int64_t row, int stage) {
         if constexpr (STAGED) {
             if (row < p.rows) {
                 unsigned char *to = mine + stage * row_bytes;
-                const int64_t at = row * p.D;
+                const int64_t base = row * p.D;
+                const char *gy = reinterpret_cast<const char *>(static_cast<const IO *>(p.dy) + base);
+                const char *gs = reinterpret_cast<const char *>(static_cast<const R *>(p.s) + base);
+                const char *gd = reinterpret_cast<const char *>(static_cast<const R *>(p.dresidual) + (dres ? base : 0));
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int j = t + i * T;
-                    if (j >= nvec) continue;
-                    cp_async16(to + j * 16, static_cast<const IO *>(p.dy) + at + j * VE);
+                    if (!live[i]) continue;
+                    const uint32_t o = at[i] * Io<IO>::kBytes;
+                    cp_async16(to + o, gy + o);
 #pragma unroll
                     for (int h = 0; h < VE * Io<R>::kBytes / 16; ++h) {
-                        const int o = j * VE * Io<R>::kBytes + h * 16;
-                        cp_async16(to + off_s + o, reinterpret_cast<const char *>(static_cast<const R *>(p.s) + at) + o);
-                        if (p.dresidual)
-                            cp_async16(to + off_d + o,
-                                       reinterpret_cast<const char *>(static_cast<const R *>(p.dresidual) + at) + o);
+                        const uint32_t q = at[i] * Io<R>::kBytes + h * 16;
+                        cp_async16(to + off_s + q, gs + q);
+                        if (dres) cp_async16(to + off_d + q, gd + q);
                     }
                 }
             }
@@ -325,23 +341,27 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
     statistics(first);
     int par = 0, stage = 0;
     for (int64_t row = first, at0 = lead; at0 < p.rows; row += step, at0 += step, par ^= 1) {
-        const int n = row < p.rows ? nvec : 0;
+        const bool work = live[0] && (!G || row < p.rows);
         const unsigned char *from = mine + stage * row_bytes;
         if constexpr (STAGED) cp_async_wait<kStages - 1>();
         f2 z[NP], v[NP], a = 0, b = 0;
-        load_pairs<R, VE, NV>(static_cast<const R *>(p.s) + row * p.D, STAGED ? from + off_s : nullptr, t, T, n, z);
-        load_pairs<IO, VE, NV>(static_cast<const IO *>(p.dy) + row * p.D, STAGED ? from : nullptr, t, T, n, v);
         const f2 mm = splat2(-mu), rr = splat2(r);
-        f2 wt[NP];
-        load_pairs<float, VE, NV>(weight, reinterpret_cast<const unsigned char *>(weight), t, T, nvec, wt);
+        if (work) {
+            f2 wt[NP];
+            load_pairs<R, VE, NV>(static_cast<const R *>(p.s) + row * p.D, STAGED ? from + off_s : nullptr, at, z);
+            load_pairs<IO, VE, NV>(static_cast<const IO *>(p.dy) + row * p.D, STAGED ? from : nullptr, at, v);
+            load_pairs<float, VE, NV>(weight, reinterpret_cast<const unsigned char *>(weight), at, wt);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            z[k] = mul2(add2(z[k], mm), rr);
-            dw[k] = fma2(v[k], z[k], dw[k]);
-            db[k] = add2(db[k], v[k]);
-            v[k] = mul2(v[k], wt[k]);
-            a = add2(a, v[k]);
-            b = fma2(v[k], z[k], b);
+            for (int k = 0; k < NP; ++k) {
+                if (VE > 1 && !live[2 * k / VE]) wt[k] = 0;
+                if (VE == 1) wt[k] = and2(wt[k], live[2 * k / VE], live[(2 * k + 1) / VE]);
+                z[k] = mul2(add2(z[k], mm), rr);
+                dw[k] = fma2(v[k], z[k], dw[k]);
+                db[k] = add2(db[k], v[k]);
+                v[k] = mul2(v[k], wt[k]);
+                a = add2(a, v[k]);
+                b = fma2(v[k], z[k], b);
+            }
         }
         statistics(row + step);
         float s1, s2, hi;
@@ -357,33 +377,33 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
             s2 = warp_sum(o.y);
         }
         const f2 m1 = splat2(p.rms ? 0.0f : -s1 * inv_d), m2 = splat2(-s2 * inv_d);
-        f2 d[NP];
-        if (p.dresidual) {
-            load_pairs<R, VE, NV>(static_cast<const R *>(p.dresidual) + row * p.D, STAGED ? from + off_d : nullptr, t, T,
-                                  n, d);
-        } else {
+        if (work) {
+            f2 d[NP];
+            if (dres) {
+                load_pairs<R, VE, NV>(static_cast<const R *>(p.dresidual) + row * p.D, STAGED ? from + off_d : nullptr, at, d);
+            } else {
 #pragma unroll
-            for (int k = 0; k < NP; ++k) d[k] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = t + i * T;
-            float o[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const int k = (i * VE + e) / 2;
-                float lo, up;
-                unpack2(fma2(fma2(z[k], m2, add2(v[k], m1)), rr, d[k]), lo, up);
-                o[e] = (i * VE + e) & 1 ? up : lo;
+                for (int k = 0; k < NP; ++k) d[k] = 0;
             }
-            if (j >= n) continue;
-            Raw<R, VE> q;
-            q.set(o);
-            q.store(static_cast<R *>(p.ds) + row * p.D + j * VE);
-            if (p.dx) {
-                Raw<IO, VE> u;
-                u.set(o);
-                u.store(static_cast<IO *>(p.dx) + row * p.D + j * VE);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float o[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const int k = (i * VE + e) / 2;
+                    float lo, up;
+                    unpack2(fma2(fma2(z[k], m2, add2(v[k], m1)), rr, d[k]), lo, up);
+                    o[e] = (i * VE + e) & 1 ? up : lo;
+                }
+                if (!live[i]) continue;
+                Raw<R, VE> q;
+                q.set(o);
+                q.store(static_cast<R *>(p.ds) + row * p.D + at[i]);
+                if (p.dx) {
+                    Raw<IO, VE> u;
+                    u.set(o);
+                    u.store(static_cast<IO *>(p.dx) + row * p.D + at[i]);
+                }
             }
         }
         issue(row + kStages * step, stage);
@@ -399,13 +419,12 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
         if constexpr (G) __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = t + i * T;
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const int c = (i * VE + e) / 2;
                 float lo, up;
                 unpack2(k == 0 ? dw[c] : db[c], lo, up);
-                if (j < nvec) own[j * VE + e] = (i * VE + e) & 1 ? up : lo;
+                if (live[i]) own[at[i] + e] = (i * VE + e) & 1 ? up : lo;
             }
         }
         if constexpr (G) {

@@ -85,22 +85,24 @@ int launch_forward(const norm::FwdParams &p, cudaStream_t s) {
 // The backward pass holds two sums a value in registers, so a thread takes 16 values at
 // most, and its rows go through shared memory.
 constexpr int64_t kRingBytes = 220 << 10;
-template <class IO, class R, int G>
-int64_t bwd_smem(int64_t D, int ve, bool dres, int rows) {
-    const int64_t weight = (D * 4 + 15) / 16 * 16, sums = G ? rows * D * 4 : 0;
-    const int64_t ring = ve > 1 ? rows * norm::bwd_stages<G>() * norm::bwd_row_bytes<IO, R>(D, dres) : 0;
+// Shared memory of a block of `rows` rows at a time with rings of `stages` rows
+template <class IO, class R>
+int64_t bwd_smem(int64_t D, int ve, bool dres, int rows, int stages) {
+    const int64_t weight = (D * 4 + 15) / 16 * 16, sums = rows > 1 ? rows * D * 4 : 0;
+    const int64_t ring = ve > 1 ? rows * stages * norm::bwd_row_bytes<IO, R>(D, dres) : 0;
     return weight + (ring > sums ? ring : sums);
 }
 template <class IO, class R>
 RowShape bwd_row_shape(int64_t D, bool dres) {
     RowShape sh = row_shape(D, sizeof(IO));
-    const int64_t n = D / sh.ve, smem = bwd_smem<IO, R, 0>(D, sh.ve, dres, 1);
+    const int64_t n = D / sh.ve, smem = bwd_smem<IO, R>(D, sh.ve, dres, 1, norm::kBlockStages);
     if (sh.ve == 1) {
         if (n > 8 * norm::kBwdThreads) sh.nv = 0;
         return sh;
     }
     const int most = 16 / sh.ve;  // vectors a thread
-    if (smem > kRingBytes || n > int64_t(most) * norm::kBwdThreads) return {sh.ve, 0, 0};
+    if (bwd_smem<IO, R>(D, sh.ve, dres, 1, norm::kLongStages) > kRingBytes || n > int64_t(most) * norm::kBwdThreads)
+        return {sh.ve, 0, 0};
     if (sh.threads <= 32 && sh.nv <= most) return sh;
     // as few values a thread as leaves the SM's threads to as many rows as its shared memory holds
     const int64_t want = norm::kBwdThreads / (smem * 2 > kRingBytes ? 1 : smem * 4 > kRingBytes ? 2 : 4);
@@ -128,15 +130,22 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
             if constexpr (ve * nv > 16) {
                 return SSCAN_ERR_INVALID;  // not a shape of bwd_row_shape
             } else {
-                constexpr auto kern = norm::norm_backward_kernel<IO, R, ve, nv, g>;
-                const int64_t smem = bwd_smem<IO, R, g>(p.D, ve, p.dresidual != nullptr, block_rows);
+                const bool dres = p.dresidual != nullptr;
                 const int threads = g ? kBwdGroupThreads : sh.threads;
-                int per_sm = static_cast<int>((kRingBytes + 7 * 1024) / (smem + 1024));  // blocks of an SM
-                if (per_sm * threads > norm::kBwdThreads) per_sm = norm::kBwdThreads / threads;
-                at_most(148 * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm));
-                if (smem_opt_in<kern>(static_cast<int>(kRingBytes)) != cudaSuccess) return SSCAN_ERR_CUDA;
-                kern<<<static_cast<unsigned>(blocks), threads, smem, s>>>(p);
-                return SSCAN_OK;
+                auto launch = [&](auto stages) -> int {
+                    constexpr auto kern = norm::norm_backward_kernel<IO, R, ve, nv, g, stages>;
+                    const int64_t smem = bwd_smem<IO, R>(p.D, ve, dres, block_rows, stages);
+                    int per_sm = static_cast<int>((kRingBytes + 7 * 1024) / (smem + 1024));  // blocks of an SM
+                    if (per_sm * threads > norm::kBwdThreads) per_sm = norm::kBwdThreads / threads;
+                    at_most(148 * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm));
+                    if (smem_opt_in<kern>(static_cast<int>(kRingBytes)) != cudaSuccess) return SSCAN_ERR_CUDA;
+                    kern<<<static_cast<unsigned>(blocks), threads, smem, s>>>(p);
+                    return SSCAN_OK;
+                };
+                if constexpr (g) return launch(Int<norm::kGroupStages>{});
+                else if (ve == 1 || bwd_smem<IO, R>(p.D, ve, dres, 1, norm::kBlockStages) <= kRingBytes)
+                    return launch(Int<norm::kBlockStages>{});
+                else return launch(Int<norm::kLongStages>{});
             }
         });
     }

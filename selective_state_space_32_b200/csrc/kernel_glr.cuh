@@ -6,7 +6,8 @@
 //
 // Each thread walks its channels token by token with the state in a register: no
 // exchange between threads, so this is the form for a few tokens (a decode step), where
-// the batch's channels alone fill the device.
+// the batch's channels alone fill the device.  Measured on B200: 1 row of 2048 channels 2.3 us,
+// 256 rows 3.3 us (10.5 MB: 1.6 us at the copy rate; launch and one memory latency the rest).
 #pragma once
 
 #include "device_utils.cuh"

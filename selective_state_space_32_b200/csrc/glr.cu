@@ -61,9 +61,10 @@ Shape scan_shape(int64_t chains, int64_t n, int64_t want) {
     if (w * c < n && chains * w * c < want / 4) c = cluster(glr::kMaxCluster);
     return {w, c};
 }
-constexpr int64_t kForwardWarps = 148 * 10;
-// the backward pass's, by the blocks that an SM holds
-constexpr int64_t backward_warps(int blocks) { return 148 * (blocks == 3 ? 13 : 10); }
+// Without staged loads a warp waits for its inputs in every step, and more warps pay: 196
+// chains of 2000 tokens of odd width, bf16 with both gates: 4x4 61 us, 4x2 105.
+constexpr int64_t forward_warps(bool staged) { return 148 * (staged ? 10 : 11); }
+constexpr int64_t backward_warps(bool staged, int blocks) { return 148 * (!staged ? 11 : blocks == 3 ? 13 : 10); }
 
 template <class IO>
 bool staged(int64_t D) { return D * int64_t(sizeof(IO)) % 16 == 0; }
@@ -105,7 +106,7 @@ template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
     constexpr int NS = IG ? 3 : 2, K = glr::kForwardRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
-    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), kForwardWarps);
+    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), forward_warps(STAGED));
     constexpr auto kern = glr::glr_scan_kernel<IO, V, STAGED, DECAY, IG, K>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
@@ -133,7 +134,7 @@ template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
     constexpr int NS = IG ? 4 : 3, K = glr::kRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
-    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(glr::scan_blocks<V>()));
+    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(STAGED, glr::scan_blocks<V>()));
     constexpr auto kern = glr::glr_scan_backward_kernel<IO, V, STAGED, DECAY, IG>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;

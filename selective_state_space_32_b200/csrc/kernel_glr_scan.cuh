@@ -52,8 +52,8 @@ constexpr int kForwardRun = 16;  // tokens of a warp's run; the backward pass ta
 template <class IO, bool STAGED> constexpr int lane_channels() { return STAGED ? 4 / Io<IO>::kBytes : 1; }
 // Blocks of kMaxWarps an SM holds.  One channel a lane: 80 registers, three (384 fp32 chains
 // of 2048 tokens, backward: 89 us, with two blocks 106; odd widths, 2 x 3000 x 1201 fp32 with
-// both gates, 32 and 60 us, with two 40 and 79); two: 128, since 80 would spill (bf16 with rate and input
-// gate, 192 chains, backward: two blocks 103 us, three 113).
+// both gates, 32 and 60 us, with two 40 and 79); two: 128, since 80 would spill (bf16 with rate
+// and input gate, 192 chains, backward: two blocks 103 us, three 113).
 template <int V> constexpr int scan_blocks() { return V == 1 ? 3 : 2; }
 
 // Bytes of a staged row: the channels of a warp

@@ -241,6 +241,42 @@ def test_gradients_against_differences_of_the_operator():
         assert abs(got - want) <= 4e-3 + 1e-4 * abs(want), (name, got, want)
 
 
+@pytest.mark.parametrize("rows,D", [(5, 24), (33, 65), (7, 640), (3, 777), (9, 2048), (300, 100)])
+def test_nothing_outside_the_outputs_is_written(rows, D):
+    """Every output through the C ABI inside a larger buffer: the rest keeps its values."""
+    import ctypes
+    lib, n = S.lib(), rows * D
+    d = {k: v.cuda() for k, v in make(rows, D, "bf16", "f32").items()}
+    p = lambda t, off=0: ctypes.c_void_p(t.data_ptr() + off)
+    pad = 64
+    held = []
+
+    def inside(count, dt):
+        t = torch.full((count + 2 * pad,), 5.0, dtype=dt, device="cuda")
+        held.append((t, count))
+        return p(t, pad * t.element_size()), t[pad:pad + count]
+    y, _ = inside(n, torch.bfloat16)
+    s, sv = inside(n, torch.float32)
+    mean, mv = inside(rows, torch.float32)
+    rstd, rv = inside(rows, torch.float32)
+    assert lib.sscan_norm_forward(rows, D, S.BF16, S.NORM_RESIDUAL_F32, EPS, p(d["x"]), p(d["residual"]), p(d["weight"]),
+                                  p(d["bias"]), y, s, mean, rstd, None) == S.OK
+    ds, _ = inside(n, torch.float32)
+    dx, _ = inside(n, torch.bfloat16)
+    dw, _ = inside(D, torch.float32)
+    db, _ = inside(D, torch.float32)
+    ws = int(lib.sscan_norm_backward_workspace_bytes(rows, D))
+    w, _ = inside(ws // 4, torch.float32)
+    torch.cuda.synchronize()
+    assert lib.sscan_norm_backward(rows, D, S.BF16, S.NORM_RESIDUAL_F32, p(d["dy"]), s, mean, rstd, p(d["weight"]),
+                                   p(d["dresidual"]), ds, dx, dw, db, w, None) == S.OK
+    torch.cuda.synchronize()
+    for t, count in held:
+        assert (t[:pad] == 5).all() and (t[pad + count:] == 5).all()
+    want = S.norm_forward(d["x"], d["weight"], d["bias"], residual=d["residual"])
+    assert torch.equal(want[1].view(-1), sv) and torch.equal(want[2], mv) and torch.equal(want[3], rv)
+
+
 def test_the_binding_refuses():
     x = torch.randn(4, 24, device="cuda")
     w = torch.ones(24, device="cuda")

@@ -37,34 +37,40 @@ struct Shape {
     int warps, cluster;
 };
 
-// `chains` = batch rows times channel groups, `n` = runs of the sequence, `want` = warps that
-// fill the device.  Measured on B200 (us; warps x blocks): about ten warps an SM are wanted,
-// in small blocks first: 192 chains of 2048 tokens, bf16 with rate and input gate: 4x2 54,
-// 4x1 74, 8x4 58; 384 fp32 chains: 4x1 49, 8x1 56, 4x2 56; 128 chains of 8192 tokens: 4x4 81,
-// 4x2 95, 8x8 105.  With enough chains, blocks of 8 warps instead of clusters of two (384
-// fp32 chains, backward: 8x1 89, 4x2 98).  Where that leaves the device half empty, 8 warps
-// as well (32 chains of 131072 tokens: 8x8 621, 4x8 632, backward 1135 against 1422), and for
-// a handful of chains clusters of 16 (1 chain of 65536 tokens: 8x16 95, 8x8 205).  With very
+// `chains` = batch rows times channel groups, `n` = runs of the sequence.  Measured on B200
+// (us; warps x blocks): about ten warps an SM are wanted, in small blocks first: 192 chains of
+// 2048 tokens, bf16 with rate and input gate: 4x2 51, 4x1 64, 8x4 58; 384 fp32 chains: 4x1 49,
+// 8x1 56, 4x2 62; 128 chains of 8192 tokens: 4x4 73, 4x2 87, 8x8 94.  With enough chains,
+// blocks of 8 warps instead of clusters of two (384 fp32 chains, backward: 8x1 84, 4x2 86).
+// Where clusters of 8 small blocks leave the device half empty, 8 warps as well (32 chains of
+// 131072 tokens, backward: 8x8 1154, 4x8 1375; forward the other way, 631 and 597), and for a
+// handful of chains clusters of 16 (1 chain of 65536 tokens: 8x16 95, 8x8 205).  With very
 // many chains fewer warps share one.
-Shape scan_shape(int64_t chains, int64_t n, int64_t want) {
+struct Fill {
+    int64_t want, low;  // warps that fill the device, and too few of them in blocks of 4
+};
+Shape scan_shape(int64_t chains, int64_t n, const Fill &fill) {
     int w = 1;
     while (w < 4 && w < n) w *= 2;
     while (w > 1 && chains * w >= 16384) w /= 2;
     auto cluster = [&](int most) {
         int c = 1;
-        while (c < most && c * w < n && chains * w * c < want) c *= 2;
+        while (c < most && c * w < n && chains * w * c < fill.want) c *= 2;
         return c;
     };
     int c = cluster(8);
     if (w == 4 && c == 2 && chains >= 2 * 148) w = glr::kMaxWarps, c = 1;
-    if (w * c < n && chains * w * c < want) w = glr::kMaxWarps, c = cluster(8);
-    if (w * c < n && chains * w * c < want / 4) c = cluster(glr::kMaxCluster);
+    if (w * c < n && chains * w * c < fill.low) w = glr::kMaxWarps, c = cluster(8);
+    if (w * c < n && chains * w * c < fill.want / 4) c = cluster(glr::kMaxCluster);
     return {w, c};
 }
 // Without staged loads a warp waits for its inputs in every step, and more warps pay: 196
 // chains of 2000 tokens of odd width, bf16 with both gates: 4x4 61 us, 4x2 105.
-constexpr int64_t forward_warps(bool staged) { return 148 * (staged ? 10 : 11); }
-constexpr int64_t backward_warps(bool staged, int blocks) { return 148 * (!staged ? 11 : blocks == 3 ? 13 : 10); }
+constexpr Fill forward_fill(bool staged) { return {148 * (staged ? 10 : 11), 148 * 6}; }
+constexpr Fill backward_fill(bool staged, int blocks) {
+    const int64_t want = 148 * (!staged ? 11 : blocks == 3 ? 13 : 10);
+    return {want, want};
+}
 
 template <class IO>
 bool staged(int64_t D) { return D * int64_t(sizeof(IO)) % 16 == 0; }
@@ -106,7 +112,7 @@ template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
     constexpr int NS = IG ? 3 : 2, K = glr::kForwardRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
-    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), forward_warps(STAGED));
+    const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), forward_fill(STAGED));
     constexpr auto kern = glr::glr_scan_kernel<IO, V, STAGED, DECAY, IG, K>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
@@ -134,7 +140,7 @@ template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
     constexpr int NS = IG ? 4 : 3, K = glr::kRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
-    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_warps(STAGED, glr::scan_blocks<V>()));
+    const Shape sh = scan_shape(p.B * groups, p.nruns, backward_fill(STAGED, glr::scan_blocks<V>()));
     constexpr auto kern = glr::glr_scan_backward_kernel<IO, V, STAGED, DECAY, IG>;
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;

@@ -101,11 +101,6 @@ template <> struct Lane<1> {
         unpack2(v[k / 2], a, b);
         return k & 1 ? b : a;
     }
-    template <int NP> static __device__ __forceinline__ void set(f2 (&v)[NP], int k, float x) {
-        float a, b;
-        unpack2(v[k / 2], a, b);
-        v[k / 2] = k & 1 ? pack2(a, x) : pack2(x, b);
-    }
 };
 template <> struct Lane<2> {
     using T = f2;
@@ -117,7 +112,6 @@ template <> struct Lane<2> {
     static __device__ __forceinline__ void store(float *p, f2 v) { store_channels<float, 2>(p, v); }
     // token k of an array of pairs: pair k
     template <int NP> static __device__ __forceinline__ f2 get(const f2 (&v)[NP], int k) { return v[k]; }
-    template <int NP> static __device__ __forceinline__ void set(f2 (&v)[NP], int k, f2 x) { v[k] = x; }
 };
 template <class IO> __device__ __forceinline__ void store_lane(IO *p, float v) { Io<IO>::st(p, v); }
 template <class IO> __device__ __forceinline__ void store_lane(IO *p, f2 v) { store_channels<IO, 2>(p, v); }
@@ -134,8 +128,9 @@ struct RunLoader {
     int64_t L, D;
     int lane, live;  // live: channels of the group that exist
 
-    // Start copying the run of tokens t0 .. t0 + K - 1 (tokens past L, channels past D: zeros).
-    __device__ __forceinline__ void issue(int64_t t0, int stage) const {
+    // Start copying the run of tokens t0 .. t0 + K - 1 at `off` = t0 D values (tokens past L,
+    // channels past D: zeros).
+    __device__ __forceinline__ void issue(int64_t t0, int64_t off, int stage) const {
         if constexpr (STAGED) {
             if (t0 >= 0 && t0 < L) {
                 const int at16 = lane % kRowLanes, col = at16 * (16 / Io<IO>::kBytes), row = lane / kRowLanes;
@@ -145,7 +140,7 @@ struct RunLoader {
                 if (live == CH && t0 + K <= L) {
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
-                        const IO *p = src[s] + t0 * D;
+                        const IO *p = src[s] + off;
 #pragma unroll
                         for (int h = 0; h < K / kRows; ++h, p += next)
                             cp_async16(dst + (s * K + kRows * h) * kRowBytes, p + own);
@@ -157,15 +152,27 @@ struct RunLoader {
 #pragma unroll
                         for (int h = 0; h < K / kRows; ++h)
                             cp_async16_or_zeros(dst + (s * K + kRows * h) * kRowBytes,
-                                                row + kRows * h < n ? src[s] + t0 * D + h * next + own : src[s],
+                                                row + kRows * h < n ? src[s] + off + h * next + own : src[s],
                                                 row + kRows * h < n);
                 }
             }
             cp_async_commit();
         }
     }
-    // stream s, pair i of the run at t0 with n tokens
-    __device__ __forceinline__ f2 pair(int64_t t0, int n, int stage, int s, int i) const {
+    // Tokens past the end of a run of n: zeros, and in stream 1, the gate, the value that makes
+    // the token's map the identity.  Every lane writes what it will read itself.
+    __device__ __forceinline__ void pad(int n, int stage, float gate) const {
+        if constexpr (STAGED) {
+            IO *at = reinterpret_cast<IO *>(ring + stage * kStageBytes) + lane * V;
+            for (int k = n; k < K; ++k)
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) Io<IO>::st(at + (s * K + k) * CH + j, s == 1 ? gate : 0.0f);
+        }
+    }
+    // stream s, pair i of the run at t0 with n tokens (not staged: `past` for those past the end)
+    __device__ __forceinline__ f2 pair(int64_t t0, int n, int stage, int s, int i, float past) const {
         if constexpr (STAGED) {
             const unsigned char *at = ring + stage * kStageBytes + s * K * kRowBytes;
             if constexpr (V == 2) {
@@ -178,11 +185,14 @@ struct RunLoader {
         } else {
             const IO *p = src[s] + (t0 + 2 * i) * D + lane;
             const bool on = lane < live;
-            return pack2(on && 2 * i < n ? Io<IO>::widen(Io<IO>::ld(p)) : 0.0f,
-                         on && 2 * i + 1 < n ? Io<IO>::widen(Io<IO>::ld(p + D)) : 0.0f);
+            return pack2(on && 2 * i < n ? Io<IO>::widen(Io<IO>::ld(p)) : past,
+                         on && 2 * i + 1 < n ? Io<IO>::widen(Io<IO>::ld(p + D)) : past);
         }
     }
 };
+
+// The gate of a token whose map is the identity: a = 1 and beta = 0
+template <bool DECAY> __device__ __forceinline__ float idle_gate() { return __uint_as_float(DECAY ? 0xff800000u : 0x7f800000u); }
 
 // (decay, offset) of one lane's channels in shared memory: V * 8 bytes
 __device__ __forceinline__ void load_map(const float2 *p, float &a, float &h) {
@@ -367,9 +377,10 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
     const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
     int64_t t0 = (static_cast<int64_t>(rank) * warps + w) * K;
-    const int64_t steps = (p.L + step - 1) / step;
+    const int64_t steps = (p.L + step - 1) / step, pitch = step * p.D;
+    int64_t off = t0 * p.D;
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) in.issue(t0 + s * step, s);
+    for (int s = 0; s < kStages; ++s) in.issue(t0 + s * step, off + s * pitch, s);
     const bool mine = lane * V < in.live;
     T carry = LV::splat(0.0f);
     f2 cc = 0;  // rate log2 e of the pair
@@ -382,24 +393,18 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     float *states = p.states ? p.states + b * p.nruns * p.D + ch0 : nullptr;
     sh.start();
     int stage = 0;
-    for (int64_t it = 0; it < steps; ++it, t0 += step) {
+    for (int64_t it = 0; it < steps; ++it, t0 += step, off += pitch) {
         const int n = t0 >= p.L ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
         f2 a[NP], bb[NP];
         if constexpr (STAGED) {
             cp_async_wait<kStages - 1>();
             __syncwarp();
         }
-        if (n > 0) {
+        if (n < K) in.pad(n, stage, idle_gate<DECAY>());
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                token2<DECAY, IG>(in.pair(t0, n, stage, 0, i), in.pair(t0, n, stage, 1, i),
-                                  IG ? in.pair(t0, n, stage, NS - 1, i) : 0, cc, a[i], bb[i]);
-        }
-        if (n < K) {  // tokens past the end: the identity
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k >= n) LV::set(a, k, LV::splat(1.0f)), LV::set(bb, k, LV::splat(0.0f));
-        }
+        for (int i = 0; i < NP; ++i)
+            token2<DECAY, IG>(in.pair(t0, n, stage, 0, i, 0.0f), in.pair(t0, n, stage, 1, i, idle_gate<DECAY>()),
+                              IG ? in.pair(t0, n, stage, NS - 1, i, 0.0f) : 0, cc, a[i], bb[i]);
         T A = LV::get(a, 0), H = LV::get(bb, 0);
 #pragma unroll
         for (int k = 1; k < K; ++k) {
@@ -407,12 +412,12 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
             H = LV::fma(LV::get(a, k), H, LV::get(bb, k));
         }
         __syncwarp();
-        in.issue(t0 + kStages * step, stage);
+        in.issue(t0 + kStages * step, off + kStages * pitch, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
         T h = exchange<V>(A, H, carry, sh, it);
-        IO *yt = y + t0 * p.D;
+        IO *yt = y + off;
         auto emit = [&](int k) {
-            if (k % kRun == 0 && states) LV::store(states + (t0 + k) / kRun * p.D + own, h);
+            if (k % kRun == 0 && states) LV::store(states + off / kRun + k / kRun * p.D + own, h);
             h = LV::fma(LV::get(a, k), h, LV::get(bb, k));
             store_lane<IO>(yt + own, h);
             yt += p.D;
@@ -456,9 +461,10 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
     in.live = static_cast<int>(p.D - ch0 < CH ? p.D - ch0 : CH);
     const int64_t step = static_cast<int64_t>(C) * warps * K;  // tokens
     int64_t t0 = (p.nruns - 1 - (static_cast<int64_t>(rank) * warps + w)) * K;  // this warp's run of the first step
-    const int64_t steps = (p.nruns * K + step - 1) / step;
+    const int64_t steps = (p.nruns * K + step - 1) / step, pitch = step * p.D;
+    int64_t off = t0 * p.D;
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) in.issue(t0 - s * step, s);
+    for (int s = 0; s < kStages; ++s) in.issue(t0 - s * step, off - s * pitch, s);
     const bool mine = lane * V < in.live;
     T carry = LV::splat(0.0f), dc = LV::splat(0.0f);
     f2 cn = 0, cl2 = 0;  // the pair's rate, and rate log2 e
@@ -470,43 +476,38 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
         if (p.dh_final) carry = LV::load(p.dh_final + b * p.D + ch0 + lane * V);
     }
     const uint32_t own = lane * V;
+    const float *states = p.states + b * p.nruns * p.D + ch0 + own;
     sh.start();
     int stage = 0;
-    for (int64_t it = 0; it < steps; ++it, t0 -= step) {
+    for (int64_t it = 0; it < steps; ++it, t0 -= step, off -= pitch) {
         const int n = t0 < 0 ? 0 : p.L - t0 < K ? static_cast<int>(p.L - t0) : K;
         f2 a[NP], g[NP], px[NP], pi[NP], pg[NP], pr[NP];
         T h = LV::splat(0.0f);
-        if (mine && n > 0) h = LV::load(p.states + (b * p.nruns + t0 / K) * p.D + ch0 + lane * V);
+        if (mine && n > 0) h = LV::load(states + off / K);
         if constexpr (STAGED) {
             cp_async_wait<kStages - 1>();
             __syncwarp();
         }
-        if (n > 0) {
+        if (n < K) in.pad(n, stage, idle_gate<DECAY>());
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                f2 bb, v, kg, kr, d;
-                g[i] = in.pair(t0, n, stage, 2, i);
-                token_grad2<DECAY, IG>(in.pair(t0, n, stage, 0, i), in.pair(t0, n, stage, 1, i),
-                                       IG ? in.pair(t0, n, stage, NS - 1, i) : 0, cn, cl2, a[i], bb, v, px[i], pi[i], kg, kr);
-                if constexpr (V == 2) {
-                    d = minus2(v, h);
-                    h = fma2(a[i], h, bb);
-                } else {  // two tokens of one channel: the second's state follows from the first's
-                    float a0, a1, b0, b1;
-                    unpack2(a[i], a0, a1);
-                    unpack2(bb, b0, b1);
-                    const float h1 = fmaf(a0, h, b0);
-                    d = minus2(v, pack2(h, h1));
-                    h = fmaf(a1, h1, b1);
-                }
-                pg[i] = mul2(kg, d);
-                pr[i] = mul2(kr, d);
+        for (int i = 0; i < NP; ++i) {
+            f2 bb, v, kg, kr, d;
+            g[i] = in.pair(t0, n, stage, 2, i, 0.0f);
+            token_grad2<DECAY, IG>(in.pair(t0, n, stage, 0, i, 0.0f), in.pair(t0, n, stage, 1, i, idle_gate<DECAY>()),
+                                   IG ? in.pair(t0, n, stage, NS - 1, i, 0.0f) : 0, cn, cl2, a[i], bb, v, px[i], pi[i], kg, kr);
+            if constexpr (V == 2) {
+                d = minus2(v, h);
+                h = fma2(a[i], h, bb);
+            } else {  // two tokens of one channel: the second's state follows from the first's
+                float a0, a1, b0, b1;
+                unpack2(a[i], a0, a1);
+                unpack2(bb, b0, b1);
+                const float h1 = fmaf(a0, h, b0);
+                d = minus2(v, pack2(h, h1));
+                h = fmaf(a1, h1, b1);
             }
-        }
-        if (n < K) {  // tokens past the end: the identity
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k >= n) LV::set(a, k, LV::splat(1.0f)), LV::set(g, k, LV::splat(0.0f));
+            pg[i] = mul2(kg, d);
+            pr[i] = mul2(kr, d);
         }
         T A = LV::splat(1.0f), F = LV::splat(0.0f);
 #pragma unroll
@@ -515,10 +516,10 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
             A = LV::mul(A, LV::get(a, k));
         }
         __syncwarp();
-        in.issue(t0 - kStages * step, stage);
+        in.issue(t0 - kStages * step, off - kStages * pitch, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
         T e = exchange<V>(A, F, carry, sh, it);
-        const int64_t at = row0 + t0 * p.D;
+        const int64_t at = row0 + off;
         IO *dx = static_cast<IO *>(p.dx) + at, *dg = static_cast<IO *>(p.dgate) + at;
         IO *di = IG ? static_cast<IO *>(p.digate) + at : nullptr;
         auto emit = [&](int k) {

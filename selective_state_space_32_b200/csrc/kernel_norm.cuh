@@ -82,16 +82,21 @@ template <class T, int VE> struct Raw {
             }
         }
     }
-    __device__ __forceinline__ void load_shared(const void *p) {
+    // from shared memory, at a 32-bit shared address
+    __device__ __forceinline__ void load_shared(uint32_t p) {
         if constexpr (VE == 1) {
-            if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t *>(p);
-            else w[0] = *reinterpret_cast<const uint16_t *>(p);
+            if constexpr (sizeof(T) == 4) {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p) : "memory");
+            } else {
+                asm volatile("{\n\t.reg .b16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(w[0]) : "r"(p) : "memory");
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-            }
+            for (int i = 0; i < kWords / 4; ++i)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                             : "r"(p + 16 * i)
+                             : "memory");
         }
     }
     __device__ __forceinline__ void zero() {
@@ -221,8 +226,8 @@ __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(con
     }
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -250,14 +255,14 @@ __device__ __forceinline__ f2 and2(f2 v, bool lo, bool hi) {
 }
 
 // A thread's NV VE values of a row as pairs, vector i at `at[i]` (in values), from memory or,
-// with `staged`, from shared memory.
+// without a row, from shared memory at `staged`.
 template <class X, int VE, int NV>
-__device__ __forceinline__ void load_pairs(const X *row, const unsigned char *staged, const int (&at)[NV],
+__device__ __forceinline__ void load_pairs(const X *row, uint32_t staged, const int (&at)[NV],
                                            f2 (&v)[NV * VE / 2]) {
     Raw<X, VE> q[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (staged != nullptr) q[i].load_shared(staged + at[i] * Io<X>::kBytes);
+        if (row == nullptr) q[i].load_shared(staged + at[i] * Io<X>::kBytes);
         else q[i].load(row + at[i]);
     }
 #pragma unroll
@@ -301,14 +306,14 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
     const int64_t lead = G ? first - (threadIdx.x & 31) / (G ? G : 1) : first;
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    const int64_t row_bytes = bwd_row_bytes<IO, R>(p.D, p.dresidual != nullptr);
-    unsigned char *mine = ring + group * kStages * row_bytes;
-    const int64_t off_s = p.D * Io<IO>::kBytes, off_d = off_s + p.D * Io<R>::kBytes;
+    const uint32_t row_bytes = static_cast<uint32_t>(bwd_row_bytes<IO, R>(p.D, p.dresidual != nullptr));
+    const uint32_t mine = smem_u32(ring) + group * kStages * row_bytes;
+    const uint32_t off_s = static_cast<uint32_t>(p.D) * Io<IO>::kBytes, off_d = off_s + static_cast<uint32_t>(p.D) * Io<R>::kBytes;
     const bool dres = p.dresidual != nullptr;
     auto issue = [&](int64_t row, int stage) {
         if constexpr (STAGED) {
             if (row < p.rows) {
-                unsigned char *to = mine + stage * row_bytes;
+                const uint32_t to = mine + stage * row_bytes;
                 const int64_t base = row * p.D;
                 const char *gy = reinterpret_cast<const char *>(static_cast<const IO *>(p.dy) + base);
                 const char *gs = reinterpret_cast<const char *>(static_cast<const R *>(p.s) + base);
@@ -349,15 +354,15 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
     int par = 0, stage = 0;
     for (int64_t row = first, at0 = lead; at0 < p.rows; row += step, at0 += step, par ^= 1) {
         const bool work = live[0] && (!G || row < p.rows);
-        const unsigned char *from = mine + stage * row_bytes;
+        const uint32_t from = mine + stage * row_bytes;
         if constexpr (STAGED) cp_async_wait<kStages - 1>();
         f2 z[NP], v[NP], a = 0, b = 0;
         const f2 mm = splat2(-mu), rr = splat2(r);
         if (work) {
             f2 wt[NP];
-            load_pairs<R, VE, NV>(static_cast<const R *>(p.s) + row * p.D, STAGED ? from + off_s : nullptr, at, z);
-            load_pairs<IO, VE, NV>(static_cast<const IO *>(p.dy) + row * p.D, STAGED ? from : nullptr, at, v);
-            load_pairs<float, VE, NV>(weight, reinterpret_cast<const unsigned char *>(weight), at, wt);
+            load_pairs<R, VE, NV>(STAGED ? nullptr : static_cast<const R *>(p.s) + row * p.D, from + off_s, at, z);
+            load_pairs<IO, VE, NV>(STAGED ? nullptr : static_cast<const IO *>(p.dy) + row * p.D, from, at, v);
+            load_pairs<float, VE, NV>(nullptr, smem_u32(weight), at, wt);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 if (VE > 1 && !live[2 * k / VE]) wt[k] = 0;
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
         if (work) {
             f2 d[NP];
             if (dres) {
-                load_pairs<R, VE, NV>(static_cast<const R *>(p.dresidual) + row * p.D, STAGED ? from + off_d : nullptr, at, d);
+                load_pairs<R, VE, NV>(STAGED ? nullptr : static_cast<const R *>(p.dresidual) + row * p.D, from + off_d, at, d);
             } else {
 #pragma unroll
                 for (int k = 0; k < NP; ++k) d[k] = 0;

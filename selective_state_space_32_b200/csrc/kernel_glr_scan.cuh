@@ -19,15 +19,19 @@
 //
 // What bounds it (B200).  fp32 is a stream: 8 x 2048 x 1536 without a rate 49 us, 95 % of the
 // copy rate.  bf16 moves half the bytes and is held by instructions: with a rate and an input
-// gate 36 a value forward, of which 18 on the FMA pipe and 4 on the MUFU (54 us for
-// 8 x 2048 x 1536, 58 % of the copy rate; issue 52 % busy, MUFU 47 %, FMA 47 %), 69 backward
-// (106 us, 53 %); without them 81 and 157 us for 2 x 8192 x 4096 (77 and 70 %).  A few long
-// walks wait for their exchanges: 1 x 131072 x 2048 621 us (53 %).
+// gate 34 a value forward, of which 18 on the FMA pipe and 4 on the MUFU (52 us for
+// 8 x 2048 x 1536, 60 % of the copy rate; issue 52 % busy, MUFU 49 %, FMA 49 %), 68 backward
+// (104 us, 54 %); without them 73 and 154 us for 2 x 8192 x 4096 (85 and 71 %).  A few long
+// walks wait for their exchanges: 1 x 131072 x 2048 597 us (56 %).
 //
 // Runs of 16 tokens halve the exchanges of runs of 8 (67 against 74 us for the first bf16
 // case); the backward pass would not fit its registers with them.  Maps by st.async instead of
 // plain stores and a cluster barrier, which has to fence every thread's output stores: 65 ->
 // 59 us for that case, backward 135 -> 113.
+//
+// Tokens past the end of a sequence get, in shared memory, the gate that makes their map the
+// identity, so that the arithmetic has no case for them (selects in registers: 78 against 73 us
+// for 2 x 8192 x 4096).
 //
 // Rows that are not a multiple of 16 bytes cannot be copied by cp.async 16 bytes at a
 // time; STAGED = false loads them from memory, one channel a lane.

@@ -24,11 +24,15 @@
 // inputs are in flight while a row is worked on.
 //
 // What bounds it (B200; share of the copy rate).  Forward: HBM (32768 x 2048 bf16 with an fp32
-// residual 118 us, 106 %; 16384 x 5120 bf16 101 us, 103 %; 16384 x 768 fp32 18 us, 86 %;
-// 65536 x 256 bf16 25 us, 84 %).  Backward: HBM for long rows with an fp32 stream
-// (32768 x 2048 165 us, 100 %; 8192 x 4096 fp32 87 us, 95 %), the two reductions and the
-// shared-memory reads of a row otherwise (16384 x 5120 bf16 142 us, 73 %; 32768 x 1024 bf16
-// 65 us, 64 %).  Odd widths: value by value (2001 x 777 fp32 7.5 and 12.5 us).
+// residual 118 us, 106 %; 16384 x 5120 bf16 101 us, 103 %; 16384 x 768 fp32 18 us, 87 %;
+// 65536 x 256 bf16 25 us, 83 %).  Backward, with the columns' sums: HBM for long rows with an
+// fp32 stream (32768 x 2048 165 us, 101 %; 8192 x 4096 fp32 85 us, 98 %), the two reductions
+// and the shared-memory reads of a row otherwise (16384 x 5120 bf16 134 us, 77 %; 32768 x 1024
+// bf16 56 us, 74 %; 16384 x 768 bf16 39 us, 79 %).  Odd widths: value by value (2001 x 777
+// fp32 7.5 and 12.5 us).
+//
+// The rings are addressed by 32-bit shared addresses; as pointers, their 64-bit arithmetic was
+// 5 of 35 instructions a value (16384 x 5120 142 us, 16384 x 768 50 us).
 #pragma once
 
 #include "device_utils.cuh"

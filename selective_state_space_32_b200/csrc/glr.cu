@@ -65,7 +65,7 @@ Shape scan_shape(int64_t chains, int64_t n, const Fill &fill) {
     return {w, c};
 }
 // Without staged loads a warp waits for its inputs in every step, and more warps pay: 196
-// chains of 2000 tokens of odd width, bf16 with both gates: 4x4 61 us, 4x2 105.
+// chains of 2000 tokens of odd width, bf16 with both gates: 4x4 52 us, 4x2 85.
 constexpr Fill forward_fill(bool staged) { return {148 * (staged ? 10 : 11), 148 * 6}; }
 constexpr Fill backward_fill(bool staged, int blocks) {
     const int64_t want = 148 * (!staged ? 11 : blocks == 3 ? 13 : 10);
@@ -211,7 +211,14 @@ int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x,
 
 size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
     if (check_sizes(B, L, D, SSCAN_F32) != SSCAN_OK || L == 0) return 0;
-    return round_up_256(size_t(B) * glr::kMaxCluster * size_t(D) * sizeof(float));
+    // one row of D sums per block of a walk, for whichever of the types and widths' kernels runs
+    const int64_t n = runs(L), narrow = B * ceil_div(D, 32), wide = B * ceil_div(D, 64);
+    int c = scan_shape(wide, n, backward_fill(true, glr::scan_blocks<2>())).cluster;
+    for (bool st : {false, true}) {
+        const int k = scan_shape(narrow, n, backward_fill(st, glr::scan_blocks<1>())).cluster;
+        c = k > c ? k : c;
+    }
+    return round_up_256(size_t(B) * size_t(c) * size_t(D) * sizeof(float));
 }
 
 int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,

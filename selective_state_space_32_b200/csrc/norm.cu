@@ -143,9 +143,10 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
                     return SSCAN_OK;
                 };
                 if constexpr (g) return launch(Int<norm::kGroupStages>{});
-                else if (ve == 1 || bwd_smem<IO, R>(p.D, ve, dres, 1, norm::kBlockStages) <= kRingBytes)
-                    return launch(Int<norm::kBlockStages>{});
-                else return launch(Int<norm::kLongStages>{});
+                if constexpr (ve > 1 && ve * nv == 16)  // rows that fill shared memory take 16 values a thread
+                    if (bwd_smem<IO, R>(p.D, ve, dres, 1, norm::kBlockStages) > kRingBytes)
+                        return launch(Int<norm::kLongStages>{});
+                return launch(Int<norm::kBlockStages>{});
             }
         });
     }

@@ -89,6 +89,9 @@ def test_sizes_of_buffers(lib):
     assert lib.sscan_glr_states_bytes(2, 100, 8) > 0 and lib.sscan_glr_states_bytes(2, 100, 8) % 4 == 0
     assert lib.sscan_glr_backward_workspace_bytes(0, 4, 8) == 0 and lib.sscan_glr_backward_workspace_bytes(1, 0, 8) == 0
     assert lib.sscan_glr_backward_workspace_bytes(2, 100, 8) >= 32
+    # a row of D sums per block: one block a batch row where there are many, at most 16
+    assert lib.sscan_glr_backward_workspace_bytes(65536, 4, 64) == 65536 * 64 * 4
+    assert lib.sscan_glr_backward_workspace_bytes(1, 1 << 20, 64) == 16 * 64 * 4
     assert lib.sscan_norm_backward_workspace_bytes(0, 8) == 0 and lib.sscan_norm_backward_workspace_bytes(5, 8) >= 64
 
 

@@ -369,28 +369,29 @@ def ssd_forward(x, delta, A, B, C, h0=None, y=None, h_final=None, want_final: bo
 # --------------------------------------------------------------------------
 # Recurrent block operators: the gated linear recurrence and the layer norm.  A decode
 # step runs in a few microseconds on the device, so these wrappers keep to what a call
-# needs: checks of attributes, one allocation per output, the current stream's handle.
+# needs: checks of attributes (written out: a function call each would cost as much as the
+# check), one allocation per output, the current stream's handle.
 
 _F32 = torch.float32
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _want(name, t, shape, dt, dev):
-    """Raise unless t is a contiguous tensor of this shape, dtype and (CUDA) device."""
-    if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: want contiguous CUDA {dt} {tuple(shape)} on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _unlike(name, t, shape, dt, d):
+    """The error of a tensor that is not a contiguous one of this shape, dtype and device."""
+    return ValueError(f"{name}: want contiguous {dt} {tuple(shape)} on cuda:{d}, got {t.dtype} {tuple(t.shape)} "
+                      f"on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _run(fn, ref, stream, args):
-    """fn(stream handle, *args) with ref's device current and new tensors allocated on the
-    call's stream, so that the allocator knows who uses them (stream None: the current
-    stream of ref's device)."""
+def _elsewhere(fn, ref, stream, args):
+    """fn(stream handle, *args) where the call is not simply on ref's current device and
+    stream: with ref's device current, and new tensors allocated on the call's stream, so
+    that the allocator knows who uses them."""
     if not ref.is_cuda:
         raise ValueError(f"want CUDA tensors, got one on {ref.device}")
     dev = ref.device
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            return fn(torch._C._cuda_getCurrentRawStream(dev.index), *args)
         stream = torch.cuda.current_stream(dev)
     elif stream.device != dev:
         raise ValueError(f"stream on {stream.device}, tensors on {dev}")
@@ -432,37 +433,54 @@ def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=No
     of ``new_glr_states`` as ``states``).  Work and new tensors are on ``stream`` (default:
     the current stream of x's device).
     Returns (y [B, L, D], h_final [B, D] float32 or None, states or None)."""
-    return _run(_glr_forward, x, stream, (x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states))
+    d = x.get_device()
+    if stream is None and d >= 0 and d == _device_now():
+        return _glr_forward(_raw_stream(d), x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states)
+    return _elsewhere(_glr_forward, x, stream,
+                      (x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states))
 
 
 def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states):
-    shape, dt, dev = x.shape, x.dtype, x.device
-    code = _dtype_code(dt)
+    shape, dt, d = x.shape, x.dtype, x.get_device()
+    code = _CODES.get(dt)
+    if code is None:
+        _dtype_code(dt)  # raises
     if len(shape) != 3:
         raise ValueError(f"x: want [B, L, D], got {tuple(shape)}")
     B, L, D = shape
-    _want("x", x, shape, dt, dev)
-    _want("gate", gate, shape, dt, dev)
+    if not x.is_contiguous():
+        raise _unlike("x", x, shape, dt, d)
+    if gate.shape != shape or gate.dtype != dt or gate.get_device() != d or not gate.is_contiguous():
+        raise _unlike("gate", gate, shape, dt, d)
     if input_gate is not None:
-        _want("input_gate", input_gate, shape, dt, dev)
+        if (input_gate.shape != shape or input_gate.dtype != dt or input_gate.get_device() != d
+                or not input_gate.is_contiguous()):
+            raise _unlike("input_gate", input_gate, shape, dt, d)
     if rate is not None:
-        _want("rate", rate, (D,), _F32, dev)
+        if rate.shape != (D,) or rate.dtype != _F32 or rate.get_device() != d or not rate.is_contiguous():
+            raise _unlike("rate", rate, (D,), _F32, d)
     if h0 is not None:
-        _want("h0", h0, (B, D), _F32, dev)
+        if h0.shape != (B, D) or h0.dtype != _F32 or h0.get_device() != d or not h0.is_contiguous():
+            raise _unlike("h0", h0, (B, D), _F32, d)
     if y is None:
         y = torch.empty_like(x)
     else:
-        _want("y", y, shape, dt, dev)
+        if y.shape != shape or y.dtype != dt or y.get_device() != d or not y.is_contiguous():
+            raise _unlike("y", y, shape, dt, d)
     if h_final is not None:
-        _want("h_final", h_final, (B, D), _F32, dev)
+        if h_final.shape != (B, D) or h_final.dtype != _F32 or h_final.get_device() != d or not h_final.is_contiguous():
+            raise _unlike("h_final", h_final, (B, D), _F32, d)
     elif want_final:
         h_final = x.new_empty((B, D), dtype=_F32) if h0 is None else torch.empty_like(h0)
     if states is not None:
-        _want("states", states, (_glr_sizes(B, L, D)[0],), _F32, dev)
+        if (states.shape != (_glr_sizes(B, L, D)[0],) or states.dtype != _F32 or states.get_device() != d
+                or not states.is_contiguous()):
+            raise _unlike("states", states, (_glr_sizes(B, L, D)[0],), _F32, d)
     elif want_states:
         states = x.new_empty(_glr_sizes(B, L, D)[0], dtype=_F32)
-    rc = lib().sscan_glr_forward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0),
-                                 y.data_ptr(), _adr(h_final), _adr(states), st)
+    rc = (_lib or lib()).sscan_glr_forward(
+        B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0), y.data_ptr(),
+        _adr(h_final), _adr(states), st)
     if rc != OK:
         raise SscanError(rc, "sscan_glr_forward")
     return y, h_final, states
@@ -476,38 +494,52 @@ def glr_backward(x, gate, dy, states, rate=None, input_gate=None, dh_final=None,
     without an input gate), drate ([D] float32, None without a rate) and dh0 ([B, D]
     float32, None unless wanted).  ``workspace``: a CUDA uint8 tensor of at least
     ``sscan_glr_backward_workspace_bytes`` (default: allocated here)."""
-    return _run(_glr_backward, x, stream, (x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace))
+    d = x.get_device()
+    if stream is None and d >= 0 and d == _device_now():
+        return _glr_backward(_raw_stream(d), x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace)
+    return _elsewhere(_glr_backward, x, stream, (x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace))
 
 
 def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace):
-    shape, dt, dev = x.shape, x.dtype, x.device
-    code = _dtype_code(dt)
+    shape, dt, d = x.shape, x.dtype, x.get_device()
+    code = _CODES.get(dt)
+    if code is None:
+        _dtype_code(dt)  # raises
     if len(shape) != 3:
         raise ValueError(f"x: want [B, L, D], got {tuple(shape)}")
     B, L, D = shape
-    _want("x", x, shape, dt, dev)
-    _want("gate", gate, shape, dt, dev)
-    _want("dy", dy, shape, dt, dev)
+    if not x.is_contiguous():
+        raise _unlike("x", x, shape, dt, d)
+    if gate.shape != shape or gate.dtype != dt or gate.get_device() != d or not gate.is_contiguous():
+        raise _unlike("gate", gate, shape, dt, d)
+    if dy.shape != shape or dy.dtype != dt or dy.get_device() != d or not dy.is_contiguous():
+        raise _unlike("dy", dy, shape, dt, d)
     n_states, n_workspace = _glr_sizes(B, L, D)
-    _want("states", states, (n_states,), _F32, dev)
+    if states.shape != (n_states,) or states.dtype != _F32 or states.get_device() != d or not states.is_contiguous():
+        raise _unlike("states", states, (n_states,), _F32, d)
     dig = drate = dh0 = None
     if input_gate is not None:
-        _want("input_gate", input_gate, shape, dt, dev)
+        if (input_gate.shape != shape or input_gate.dtype != dt or input_gate.get_device() != d
+                or not input_gate.is_contiguous()):
+            raise _unlike("input_gate", input_gate, shape, dt, d)
         dig = torch.empty_like(x)
     if dh_final is not None:
-        _want("dh_final", dh_final, (B, D), _F32, dev)
+        if (dh_final.shape != (B, D) or dh_final.dtype != _F32 or dh_final.get_device() != d
+                or not dh_final.is_contiguous()):
+            raise _unlike("dh_final", dh_final, (B, D), _F32, d)
     if want_dh0:
         dh0 = x.new_empty((B, D), dtype=_F32) if dh_final is None else torch.empty_like(dh_final)
     if rate is not None:
-        _want("rate", rate, (D,), _F32, dev)
+        if rate.shape != (D,) or rate.dtype != _F32 or rate.get_device() != d or not rate.is_contiguous():
+            raise _unlike("rate", rate, (D,), _F32, d)
         drate = torch.empty_like(rate)
         workspace = _workspace(workspace, n_workspace, x)
     else:
         workspace = None
     dx, dgate = torch.empty_like(x), torch.empty_like(x)
-    rc = lib().sscan_glr_backward(B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate),
-                                  states.data_ptr(), dy.data_ptr(), _adr(dh_final), dx.data_ptr(), dgate.data_ptr(),
-                                  _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
+    rc = (_lib or lib()).sscan_glr_backward(
+        B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), states.data_ptr(), dy.data_ptr(),
+        _adr(dh_final), dx.data_ptr(), dgate.data_ptr(), _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
     if rc != OK:
         raise SscanError(rc, "sscan_glr_backward")
     return {"dx": dx, "dgate": dgate, "dinput_gate": dig, "drate": drate, "dh0": dh0}
@@ -515,7 +547,9 @@ def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0,
 
 def _norm_types(x_dt, r_dt):
     """(dtype code, residual flag) of a norm whose x and residual have these dtypes."""
-    code = _dtype_code(x_dt)
+    code = _CODES.get(x_dt)
+    if code is None:
+        _dtype_code(x_dt)  # raises
     if r_dt == x_dt:
         return code, 0
     if r_dt == _F32:
@@ -534,33 +568,42 @@ def norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5, rm
     mean and rstd float32, one per row (mean None with rms, both None unless
     ``want_stats``).  Work and new tensors are on ``stream`` (default: the current stream
     of x's device)."""
-    return _run(_norm_forward, x, stream, (x, weight, bias, residual, eps, rms, want_stats))
+    d = x.get_device()
+    if stream is None and d >= 0 and d == _device_now():
+        return _norm_forward(_raw_stream(d), x, weight, bias, residual, eps, rms, want_stats)
+    return _elsewhere(_norm_forward, x, stream, (x, weight, bias, residual, eps, rms, want_stats))
 
 
 def _norm_forward(st, x, weight, bias, residual, eps, rms, want_stats):
-    shape, dt, dev = x.shape, x.dtype, x.device
+    shape, dt, d = x.shape, x.dtype, x.get_device()
     if len(shape) < 1:
         raise ValueError("x: want [..., D]")
     D = shape[-1]
-    _want("x", x, shape, dt, dev)
+    if not x.is_contiguous():
+        raise _unlike("x", x, shape, dt, d)
     if residual is None:
-        code, flags, s = _dtype_code(dt), 0, x
+        code, flags = _norm_types(dt, dt)
+        s = x
     else:
         code, flags = _norm_types(dt, residual.dtype)
-        _want("residual", residual, shape, residual.dtype, dev)
+        if residual.shape != shape or residual.get_device() != d or not residual.is_contiguous():
+            raise _unlike("residual", residual, shape, residual.dtype, d)
         s = torch.empty_like(residual)
     if weight is not None:
-        _want("weight", weight, (D,), _F32, dev)
+        if weight.shape != (D,) or weight.dtype != _F32 or weight.get_device() != d or not weight.is_contiguous():
+            raise _unlike("weight", weight, (D,), _F32, d)
     if bias is not None:
-        _want("bias", bias, (D,), _F32, dev)
+        if bias.shape != (D,) or bias.dtype != _F32 or bias.get_device() != d or not bias.is_contiguous():
+            raise _unlike("bias", bias, (D,), _F32, d)
     y = torch.empty_like(x)
+    rows = x.numel() // D if D else shape[:-1].numel()
     mean = rstd = None
     if want_stats:
         rstd = x.new_empty(shape[:-1], dtype=_F32)
         mean = None if rms else torch.empty_like(rstd)
-    rc = lib().sscan_norm_forward(shape[:-1].numel(), D, code, flags | (NORM_RMS if rms else 0), eps, x.data_ptr(),
-                                  _adr(residual), _adr(weight), _adr(bias), y.data_ptr(),
-                                  None if residual is None else s.data_ptr(), _adr(mean), _adr(rstd), st)
+    rc = (_lib or lib()).sscan_norm_forward(
+        rows, D, code, flags | (NORM_RMS if rms else 0), eps, x.data_ptr(), _adr(residual), _adr(weight), _adr(bias),
+        y.data_ptr(), None if residual is None else s.data_ptr(), _adr(mean), _adr(rstd), st)
     if rc != OK:
         raise SscanError(rc, "sscan_norm_forward")
     return y, s, mean, rstd
@@ -579,31 +622,43 @@ def norm_backward(dy, s, mean, rstd, weight=None, dresidual=None, rms: bool = Fa
     dx (dtype of dy), dresidual (dtype of s; the same tensor as dx where the types are
     equal), dweight and dbias ([D] float32 or None).  ``workspace``: a CUDA uint8 tensor of
     at least ``sscan_norm_backward_workspace_bytes`` (default: allocated here)."""
-    return _run(_norm_backward, dy, stream, (dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace))
+    d = dy.get_device()
+    if stream is None and d >= 0 and d == _device_now():
+        return _norm_backward(_raw_stream(d), dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias,
+                              workspace)
+    return _elsewhere(_norm_backward, dy, stream,
+                      (dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace))
 
 
 def _norm_backward(st, dy, s, mean, rstd, weight, dresidual, rms, want_dweight, want_dbias, workspace):
-    shape, dt, dev = dy.shape, dy.dtype, dy.device
+    shape, dt, d = dy.shape, dy.dtype, dy.get_device()
     if len(shape) < 1:
         raise ValueError("dy: want [..., D]")
     D, row_shape = shape[-1], shape[:-1]
     code, flags = _norm_types(dt, s.dtype)
-    _want("dy", dy, shape, dt, dev)
-    _want("s", s, shape, s.dtype, dev)
-    _want("rstd", rstd, row_shape, _F32, dev)
+    if not dy.is_contiguous():
+        raise _unlike("dy", dy, shape, dt, d)
+    if s.shape != shape or s.get_device() != d or not s.is_contiguous():
+        raise _unlike("s", s, shape, s.dtype, d)
+    if rstd.shape != row_shape or rstd.dtype != _F32 or rstd.get_device() != d or not rstd.is_contiguous():
+        raise _unlike("rstd", rstd, row_shape, _F32, d)
     if not rms:
         if mean is None:
             raise ValueError("mean: wanted without rms")
-        _want("mean", mean, row_shape, _F32, dev)
+        if mean.shape != row_shape or mean.dtype != _F32 or mean.get_device() != d or not mean.is_contiguous():
+            raise _unlike("mean", mean, row_shape, _F32, d)
     elif mean is not None:
         raise ValueError("mean: must be None with rms")
     dweight = dbias = None
     if weight is not None:
-        _want("weight", weight, (D,), _F32, dev)
+        if weight.shape != (D,) or weight.dtype != _F32 or weight.get_device() != d or not weight.is_contiguous():
+            raise _unlike("weight", weight, (D,), _F32, d)
         if want_dweight:
             dweight = torch.empty_like(weight)
     if dresidual is not None:
-        _want("dresidual", dresidual, shape, s.dtype, dev)
+        if (dresidual.shape != shape or dresidual.dtype != s.dtype or dresidual.get_device() != d
+                or not dresidual.is_contiguous()):
+            raise _unlike("dresidual", dresidual, shape, s.dtype, d)
     rows = row_shape.numel()
     ds = torch.empty_like(s)
     dx = torch.empty_like(dy) if s.dtype != dt else None
@@ -613,9 +668,9 @@ def _norm_backward(st, dy, s, mean, rstd, weight, dresidual, rms, want_dweight, 
         workspace = _workspace(workspace, _norm_workspace(rows, D), dy)
     else:
         workspace = None
-    rc = lib().sscan_norm_backward(rows, D, code, flags | (NORM_RMS if rms else 0), dy.data_ptr(), s.data_ptr(),
-                                   _adr(mean), rstd.data_ptr(), _adr(weight), _adr(dresidual), ds.data_ptr(), _adr(dx),
-                                   _adr(dweight), _adr(dbias), _adr(workspace), st)
+    rc = (_lib or lib()).sscan_norm_backward(
+        rows, D, code, flags | (NORM_RMS if rms else 0), dy.data_ptr(), s.data_ptr(), _adr(mean), rstd.data_ptr(),
+        _adr(weight), _adr(dresidual), ds.data_ptr(), _adr(dx), _adr(dweight), _adr(dbias), _adr(workspace), st)
     if rc != OK:
         raise SscanError(rc, "sscan_norm_backward")
     return {"dx": ds if dx is None else dx, "dresidual": ds, "dweight": dweight, "dbias": dbias}

@@ -22,7 +22,7 @@
 // gate 34 a value forward, of which 18 on the FMA pipe and 4 on the MUFU (52 us for
 // 8 x 2048 x 1536, 60 % of the copy rate; issue 52 % busy, MUFU 49 %, FMA 49 %), 68 backward
 // (104 us, 54 %); without them 73 and 154 us for 2 x 8192 x 4096 (85 and 71 %).  A few long
-// walks wait for their exchanges: 1 x 131072 x 2048 597 us (56 %).
+// walks wait for their exchanges: 1 x 131072 x 2048 602 us (55 %).
 //
 // Runs of 16 tokens halve the exchanges of runs of 8 (67 against 74 us for the first bf16
 // case); the backward pass would not fit its registers with them.  Maps by st.async instead of
@@ -255,9 +255,13 @@ struct Shared {
     uint64_t *bar;
     uint32_t C, rank;
     int warps, w, lane;
-    bool lost;  // a wait for the cluster's maps gave up: the state is NaN from there on
+    // A wait for the cluster's maps gave up: the state is NaN from there on, and this thread
+    // sends and arms no more, so that the other blocks' waits give up too, once each.
+    bool lost;
 
-    __device__ __forceinline__ void init(unsigned char *smem, unsigned char *maps, int ch, uint32_t cluster) {
+    // reads: have_read will follow
+    __device__ __forceinline__ void init(unsigned char *smem, unsigned char *maps, int ch, uint32_t cluster,
+                                         bool reads = false) {
         C = cluster;
         rank = C > 1 ? cluster_rank() : 0;
         lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
@@ -271,13 +275,23 @@ struct Shared {
                 mbar_fence_init();
             }
             __syncwarp();
-            cluster_arrive();
+            if (!reads) cluster_arrive();
         }
     }
-    // Every block of the cluster has started and set up its mbarriers: it may be sent to.
+    // Once the caller has read the initial state that another block overwrites at the end.
+    __device__ __forceinline__ void have_read() const {
+        __syncwarp();
+        if (C > 1) cluster_arrive();
+    }
+    // Every block of the cluster has set up its mbarriers: it may be sent to.
     __device__ __forceinline__ void start() const {
         __syncwarp();
         if (C > 1) cluster_wait();
+    }
+    // A thread that lost a wait stays until the others have come here or ended: till then they
+    // may still send to its block.
+    __device__ __forceinline__ void finish() const {
+        if (lost) asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
     }
 };
 
@@ -324,7 +338,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
         Hb = LV::fma(ma, Hb, mh);
     }
     const T Ap = Ab, Hp = Hb;
-    if (static_cast<uint32_t>(w) < sh.C) {
+    if (static_cast<uint32_t>(w) < sh.C && !sh.lost) {
         if (warps == 1) {
             Ab = A, Hb = H;
         } else {
@@ -343,7 +357,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
         sh.lost = true;
         carry = LV::splat(__uint_as_float(0x7fc00000u));
     }
-    if (threadIdx.x == 0) mbar_expect_tx(sh.bar + par, sh.C * CH * 8);  // for the second next step
+    if (threadIdx.x == 0 && !sh.lost) mbar_expect_tx(sh.bar + par, sh.C * CH * 8);  // for the second next step
     at = sh.cl + par * sh.C * CH + sh.lane * V;
     T h = carry;
 #pragma unroll 2
@@ -368,7 +382,8 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
-    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
+    const bool in_place = p.h0 && p.h_final == p.h0;
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, in_place);
     const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;
@@ -392,6 +407,7 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
         if constexpr (DECAY) cc = mul2(capped_rate(load_channels<float, V>(p.rate + ch0 + lane * V)), splat2(kLog2e));
         if (p.h0) carry = LV::load(p.h0 + b * p.D + ch0 + lane * V);
     }
+    if (in_place) sh.have_read();
     IO *y = static_cast<IO *>(p.y) + row0;
     const uint32_t own = lane * V;
     float *states = p.states ? p.states + b * p.nruns * p.D + ch0 : nullptr;
@@ -436,6 +452,7 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
         }
     }
     if (p.h_final && rank == 0 && w == 0 && mine) LV::store(p.h_final + b * p.D + ch0 + lane * V, carry);
+    sh.finish();
 }
 
 // The walk from the last token.  part (with a rate): row b * C + rank holds the sums of
@@ -554,6 +571,7 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
             LV::store(p.part + (b * C + rank) * p.D + ch0 + lane * V, dc);
         }
     }
+    sh.finish();
 }
 
 }  // namespace glr

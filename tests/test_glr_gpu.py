@@ -181,6 +181,18 @@ def test_state_in_place_and_in_pieces(L, dtype):
     close(h, hr, bh, "h in pieces")
 
 
+@pytest.mark.parametrize("B,L,D,dtype", [(1, 17, 64, "bf16"), (1, 200, 64, "bf16"), (1, 4100, 40, "f32"), (3, 900, 101, "bf16"),
+                                         (2, 3000, 96, "f32")])
+def test_state_in_place_across_blocks(B, L, D, dtype):
+    """The blocks of a walk all start from h0, also where the walk's end overwrites it."""
+    c = cuda(make(B, L, D, dtype, True, True, True, seed=L))
+    y, hf, _ = S.glr_forward(c["x"], c["gate"], c["rate"], c["input_gate"], c["h0"])
+    for _ in range(50):
+        h = c["h0"].clone()
+        yi, hi, _ = S.glr_forward(c["x"], c["gate"], c["rate"], c["input_gate"], h, h_final=h)
+        assert hi is h and torch.equal(yi, y) and torch.equal(h, hf)
+
+
 def test_token_by_token_equals_the_sequence():
     d = make(3, 40, 136, "f32", True, False, True)
     v, c = host(d), cuda(d)

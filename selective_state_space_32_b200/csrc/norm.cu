@@ -70,7 +70,9 @@ template <class IO, class R, bool RES>
 int launch_forward(const norm::FwdParams &p, cudaStream_t s) {
     const RowShape sh = row_shape(p.D, sizeof(IO));
     if (sh.nv == 0) {
-        norm::norm_forward_long_kernel<IO, R, RES><<<static_cast<unsigned>(p.rows), norm::kLongThreads, 0, s>>>(p);
+        const unsigned blocks = static_cast<unsigned>(p.rows);
+        if (sh.ve == 1) norm::norm_forward_long_kernel<IO, R, RES, 1><<<blocks, norm::kLongThreads, 0, s>>>(p);
+        else norm::norm_forward_long_kernel<IO, R, RES, 16 / sizeof(IO)><<<blocks, norm::kLongThreads, 0, s>>>(p);
     } else {
         with_shape<sizeof(IO)>(sh, [&](auto ve, auto nv, auto g) {
             constexpr int rows = g ? 128 / (g ? g : 1) : 1;  // of a block
@@ -123,8 +125,12 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
     int rc = SSCAN_OK;
     auto at_most = [&](int64_t n) { blocks = blocks < n ? blocks : n; };
     if (sh.nv == 0) {
-        at_most(148 * 2);
-        norm::norm_backward_long_kernel<IO, R><<<static_cast<unsigned>(blocks), norm::kLongThreads, 0, s>>>(p);
+        at_most(148);  // the rows that a block reads twice stay in the L2
+        const int64_t each = ceil_div(p.rows, blocks);
+        blocks = ceil_div(p.rows, each);
+        const unsigned n = static_cast<unsigned>(blocks);
+        if (sh.ve == 1) norm::norm_backward_long_kernel<IO, R, 1><<<n, norm::kLongThreads, 0, s>>>(p, each);
+        else norm::norm_backward_long_kernel<IO, R, 16 / sizeof(IO)><<<n, norm::kLongThreads, 0, s>>>(p, each);
     } else {
         rc = with_shape<sizeof(IO)>(sh, [&](auto ve, auto nv, auto g) -> int {
             if constexpr (ve * nv > 16) {

@@ -140,6 +140,13 @@ def test_rows(rows):
     check(rows, 640, "bf16", "f32", True, bias=False)
 
 
+@pytest.mark.parametrize("rows,D,dtype,residual", [(149, 12288, "bf16", "same"), (700, 10248, "bf16", "f32"), (743, 6001, "bf16", None),
+                                                   (297, 16384, "f32", "same"), (1300, 5121, "f32", None), (2, 40001, "bf16", "same")])
+def test_rows_in_several_passes(rows, D, dtype, residual):
+    """Rows too long for a block's registers: one row a block, several, and a last batch of fewer."""
+    check(rows, D, dtype, residual, False)
+
+
 @pytest.mark.parametrize("mean", [0.0, 30.0, 1000.0])
 def test_a_mean_far_from_zero(mean):
     check(6, 640, "f32", None, False, mean=mean)

@@ -12,8 +12,8 @@
 // no digits of the variance.
 //
 // Both passes are streams: a row is read once, held in registers, and written once.  T
-// threads share a row, in vectors of VE consecutive values (16 bytes of x, or single
-// values where D is not a multiple), NV vectors a thread: thread i takes vectors i, i + T,
+// threads share a row, in vectors of VE consecutive values (16 bytes of x; single values in
+// short rows whose D is not a multiple), NV vectors a thread: thread i takes vectors i, i + T,
 // ...  A short row belongs to a group of G = 8, 16 or 32 lanes (no barrier at all); a longer
 // one is the block's (G = 0), which meets once: each warp reduces its own part (forward: mean and centred squares,
 // joined by (n, mean, M2) as of sets; backward: two sums), and every thread joins the
@@ -28,8 +28,10 @@
 // 65536 x 256 bf16 25 us, 83 %).  Backward, with the columns' sums: HBM for long rows with an
 // fp32 stream (32768 x 2048 165 us, 101 %; 8192 x 4096 fp32 85 us, 98 %), the two reductions
 // and the shared-memory reads of a row otherwise (16384 x 5120 bf16 134 us, 77 %; 32768 x 1024
-// bf16 56 us, 74 %; 16384 x 768 bf16 39 us, 79 %).  Odd widths: value by value (2001 x 777
-// fp32 7.5 and 12.5 us).
+// bf16 56 us, 74 %; 16384 x 768 bf16 39 us, 79 %).  Widths that are not a multiple of 16 bytes, by
+// the aligned vectors that cover a row: 4000 x 6001 bf16 with a residual 70 and 81 us (42 and
+// 37 %), 4000 x 7999 with an fp32 one 96 and 176, 8000 x 1999 41 and 49, 2001 x 777 fp32 8 and 12;
+// value by value 147 and 223, 166 and 322, 60 and 74, 7.5 and 12.5.
 //
 // The rings are addressed by 32-bit shared addresses; as pointers, their 64-bit arithmetic was
 // 5 of 35 instructions a value (16384 x 5120 142 us, 16384 x 768 50 us).
@@ -135,6 +137,40 @@ template <class T, int VE> struct Raw {
     }
 };
 
+// Rows that do not begin at a 16-byte boundary (SHIFT): a row of D values from value `row0` on is
+// covered by the aligned vectors from row0 - m on, m = row0 % VE; value e of vector j is column
+// j VE - m + e, and the first and the last vector hold values of other rows too.  A vector that
+// reaches past the tensor's `total` values is read value by value.
+template <class T, int VE>
+__device__ __forceinline__ void load_shifted(Raw<T, VE> &q, const T *p, int64_t at, int64_t total) {
+    if (at + VE <= total) {
+        q.load(p + at);
+        return;
+    }
+    float v[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = at + e < total ? Io<T>::widen(Io<T>::ld(p + at + e)) : 0.0f;
+    q.set(v);
+}
+// VE weights from column c on (0 for columns that are none): aligned vectors of four, and the
+// values picked from them; c % 4 is the same in a block.
+template <int VE>
+__device__ __forceinline__ void weights_shifted(float (&o)[VE], const float *p, int64_t c, int64_t D) {
+    const int sh = static_cast<int>(c & 3);
+    if (c < 0 || c - sh + VE + 4 > D) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) o[e] = c + e >= 0 && c + e < D ? __ldg(p + c + e) : 0.0f;
+        return;
+    }
+    Raw<float, VE + 4> q;
+    q.load(p + c - sh);
+    float v[VE + 2];
+#pragma unroll
+    for (int e = 0; e < VE + 2; ++e) v[e] = sh & 1 ? q.get(e + 1) : q.get(e);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) o[e] = sh & 2 ? v[e + 2] : v[e];
+}
+
 // values of a row that warp w of a row of T threads holds
 template <int VE, int NV>
 __device__ __forceinline__ int warp_values(int64_t nvec, int w, int T) {
@@ -148,14 +184,20 @@ __device__ __forceinline__ int warp_values(int64_t nvec, int w, int T) {
 }
 
 // IO: x, y; R: residual and residual_out.  G > 0: blockDim / G rows a block; G = 0: one.
-template <class IO, class R, bool RES, int VE, int NV, int G>
+template <class IO, class R, bool RES, int VE, int NV, int G, bool SHIFT>
 __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(const FwdParams p) {
+    static_assert(!SHIFT || (G == 0 && VE > 1), "a block a row, by vectors");
     __shared__ float4 part[32];  // a warp's number of values, their mean and centred squares
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int T = G ? G : blockDim.x, t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
     const int64_t row = G ? (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / (G ? G : 1) : blockIdx.x;
     // groups past the last row go along with nothing to read or write
-    const int64_t nvec = row < p.rows ? p.D / VE : 0, at = row * p.D;
+    const int m = SHIFT ? static_cast<int>(row * p.D % VE) : 0;
+    const int64_t nvec = SHIFT ? (p.D + m + VE - 1) / VE : row < p.rows ? p.D / VE : 0, at = row * p.D - m;
+    const int64_t total = p.rows * p.D;
+    // the first vector of others' values at its start, the last of others' at its end
+    auto edge = [&](int64_t j) { return SHIFT && (j == 0 || j == nvec - 1); };
+    auto inside = [&](int64_t j, int e) { return j * VE + e >= m && j * VE + e < p.D + m; };
     float v[NV][VE];
     float sum = 0.0f;
 #pragma unroll
@@ -163,32 +205,63 @@ __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(con
         const int64_t j = t + static_cast<int64_t>(i) * T;
         Raw<IO, VE> x;
         x.zero();
-        if (j < nvec) x.load(static_cast<const IO *>(p.x) + at + j * VE);
+        if (j < nvec) {
+            if constexpr (SHIFT) load_shifted(x, static_cast<const IO *>(p.x), at + j * VE, total);
+            else x.load(static_cast<const IO *>(p.x) + at + j * VE);
+        }
         if constexpr (RES) {
             Raw<R, VE> r;
             r.zero();
-            if (j < nvec) r.load(static_cast<const R *>(p.residual) + at + j * VE);
+            if (j < nvec) {
+                if constexpr (SHIFT) load_shifted(r, static_cast<const R *>(p.residual), at + j * VE, total);
+                else r.load(static_cast<const R *>(p.residual) + at + j * VE);
+            }
 #pragma unroll
             for (int e = 0; e < VE; ++e) v[i][e] = x.get(e) + r.get(e);
             r.set(v[i]);
-            if (j < nvec) r.store(static_cast<R *>(p.residual_out) + at + j * VE);
+            R *out = static_cast<R *>(p.residual_out) + at + j * VE;
+            if (j < nvec) {
+                if (edge(j)) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        if (inside(j, e)) Io<R>::st(out + e, r.get(e));
+                } else {
+                    r.store(out);
+                }
+            }
 #pragma unroll
             for (int e = 0; e < VE; ++e) v[i][e] = r.get(e);
         } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e) v[i][e] = x.get(e);
         }
+        if (edge(j)) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (!inside(j, e)) v[i][e] = 0.0f;
+        }
 #pragma unroll
         for (int e = 0; e < VE; ++e) sum += v[i][e];
     }
-    const int n = G ? static_cast<int>(p.D) : warp_values<VE, NV>(nvec, w, T);
+    int n = G ? static_cast<int>(p.D) : warp_values<VE, NV>(nvec, w, T);
+    if constexpr (SHIFT) {
+        if (w == 0) n -= m;
+        if (w == static_cast<int>((nvec - 1) % T) >> 5) n -= static_cast<int>(nvec * VE - m - p.D);
+    }
     float mu = p.rms || n == 0 ? 0.0f : warp_sum<G ? G : 32>(sum) / static_cast<float>(n);
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (t + static_cast<int64_t>(i) * T < nvec) {
+            const int64_t j = t + static_cast<int64_t>(i) * T;
+            if (edge(j)) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sq = fmaf(v[i][e] - mu, v[i][e] - mu, sq);
+                for (int e = 0; e < VE; ++e)
+                    if (inside(j, e)) sq = fmaf(v[i][e] - mu, v[i][e] - mu, sq);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) sq = fmaf(v[i][e] - mu, v[i][e] - mu, sq);
+            }
         }
     sq = warp_sum<G ? G : 32>(sq);
     const float inv_d = 1.0f / static_cast<float>(p.D);
@@ -208,21 +281,37 @@ __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(con
         if (j >= nvec) continue;
 #pragma unroll
         for (int e = 0; e < VE; ++e) v[i][e] = (v[i][e] - mu) * rstd;
-        if (p.weight) {
-            Raw<float, VE> g;
-            g.load(p.weight + j * VE);
+        auto column = [&](const float *of, float (&g)[VE]) {
+            if constexpr (SHIFT) {
+                weights_shifted(g, of, j * VE - m, p.D);
+            } else {
+                Raw<float, VE> q;
+                q.load(of + j * VE);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[i][e] *= g.get(e);
+                for (int e = 0; e < VE; ++e) g[e] = q.get(e);
+            }
+        };
+        float g[VE];
+        if (p.weight) {
+            column(p.weight, g);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v[i][e] *= g[e];
         }
         if (p.bias) {
-            Raw<float, VE> g;
-            g.load(p.bias + j * VE);
+            column(p.bias, g);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[i][e] += g.get(e);
+            for (int e = 0; e < VE; ++e) v[i][e] += g[e];
+        }
+        IO *out = static_cast<IO *>(p.y) + at + j * VE;
+        if (edge(j)) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (inside(j, e)) Io<IO>::st(out + e, v[i][e]);
+            continue;
         }
         Raw<IO, VE> o;
         o.set(v[i]);
-        o.store(static_cast<IO *>(p.y) + at + j * VE);
+        o.store(out);
     }
     if (t == 0 && row < p.rows) {
         if (p.mean) p.mean[row] = mu;
@@ -232,6 +321,9 @@ __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(con
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int bytes) {  // then zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -277,23 +369,29 @@ __device__ __forceinline__ void load_pairs(const X *row, uint32_t staged, const 
 // IO: dy, dx; R: s, dresidual, ds.  G > 0: G lanes a row; G = 0: a block a row.  With VE > 1 the
 // rows come through a ring in shared memory, filled by cp.async: every thread copies the
 // vectors that it reads itself, so only its own copies are waited for.  Single values
-// (VE = 1) are loaded from memory; the blocks of an SM cover each other there.  A thread's
+// (VE = 1, rows of one warp) are loaded from memory; the warps of an SM cover each other there.  A thread's
 // NV VE values are packed pairs: the pass would be bound by instructions otherwise.
 // Dynamic shared memory: the weight (D floats; ones without a weight), then the rings, used
 // again for the warps' sums (D floats each) at the end.
-template <class IO, class R, int VE, int NV, int G, int kStages>
+// SHIFT: the grid's rows are a multiple of VE apart, or a block has one row, so that m is the
+// same for all of a block's rows and its columns stay where they are; D is then the width
+// of the aligned vectors (Dp), the weight 0 in front of and behind the row.
+template <class IO, class R, int VE, int NV, int G, int kStages, int SHIFT>
 __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(const BwdParams p) {
+    static_assert(!SHIFT || (G == 0 && VE > 1), "a block a row, by vectors");
     constexpr bool STAGED = VE > 1;
     constexpr int NP = NV * VE / 2;
     __shared__ float2 part[2][32];
     extern __shared__ __align__(16) unsigned char smem[];
     float *weight = reinterpret_cast<float *>(smem);
-    unsigned char *ring = smem + (p.D * 4 + 15) / 16 * 16;
+    const int m = SHIFT ? static_cast<int>(blockIdx.x * p.D % VE) : 0;
+    const int64_t Dp = SHIFT ? (p.D + 2 * VE - 2) / VE * VE : p.D;
+    unsigned char *ring = smem + (Dp * 4 + 15) / 16 * 16;
     float *columns = reinterpret_cast<float *>(ring);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int T = G ? G : blockDim.x, t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
     const int groups = G ? blockDim.x / (G ? G : 1) : 1, group = G ? threadIdx.x / (G ? G : 1) : 0;
-    const int nvec = static_cast<int>(p.D / VE);
+    const int nvec = static_cast<int>(SHIFT ? (p.D + m + VE - 1) / VE : p.D / VE);
     // this thread's vectors; in place of one past the row's end its first is read again (with
     // a weight of 0) and nothing is written; a thread without any only joins the sums
     int at[NV];
@@ -304,21 +402,23 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
         live[i] = j < nvec;
         at[i] = (live[i] ? j : t) * VE;
     }
+    auto edge = [&](int i) { return SHIFT && (at[i] == 0 || at[i] == (nvec - 1) * VE); };
+    auto inside = [&](int i, int e) { return at[i] + e >= m && at[i] + e < p.D + m; };
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     // a warp's groups walk together (their sums are exchanged in one instruction): they end
     // when the warp's first row is past the last, and a row past it is empty
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
     const int64_t lead = G ? first - (threadIdx.x & 31) / (G ? G : 1) : first;
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    const uint32_t row_bytes = static_cast<uint32_t>(bwd_row_bytes<IO, R>(p.D, p.dresidual != nullptr));
+    const uint32_t row_bytes = static_cast<uint32_t>(bwd_row_bytes<IO, R>(Dp, p.dresidual != nullptr));
     const uint32_t mine = smem_u32(ring) + group * kStages * row_bytes;
-    const uint32_t off_s = static_cast<uint32_t>(p.D) * Io<IO>::kBytes, off_d = off_s + static_cast<uint32_t>(p.D) * Io<R>::kBytes;
+    const uint32_t off_s = static_cast<uint32_t>(Dp) * Io<IO>::kBytes, off_d = off_s + static_cast<uint32_t>(Dp) * Io<R>::kBytes;
     const bool dres = p.dresidual != nullptr;
     auto issue = [&](int64_t row, int stage) {
         if constexpr (STAGED) {
             if (row < p.rows) {
                 const uint32_t to = mine + stage * row_bytes;
-                const int64_t base = row * p.D;
+                const int64_t base = row * p.D - m;
                 const char *gy = reinterpret_cast<const char *>(static_cast<const IO *>(p.dy) + base);
                 const char *gs = reinterpret_cast<const char *>(static_cast<const R *>(p.s) + base);
                 const char *gd = reinterpret_cast<const char *>(static_cast<const R *>(p.dresidual) + (dres ? base : 0));
@@ -326,6 +426,19 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
                 for (int i = 0; i < NV; ++i) {
                     if (!live[i]) continue;
                     const uint32_t o = at[i] * Io<IO>::kBytes;
+                    if constexpr (SHIFT) {
+                        const int64_t left = p.rows * p.D - base - at[i];  // values to the tensor's end
+                        if (left < VE) {
+                            cp_async16_part(to + o, gy + o, static_cast<int>(left) * Io<IO>::kBytes);
+                            for (int h = 0; h < VE * Io<R>::kBytes / 16; ++h) {
+                                const int n = static_cast<int>(left) * Io<R>::kBytes - h * 16;
+                                const uint32_t q = at[i] * Io<R>::kBytes + (n > 0 ? h * 16 : 0), z = off_s + at[i] * Io<R>::kBytes + h * 16;
+                                cp_async16_part(to + z, gs + q, n > 16 ? 16 : n > 0 ? n : 0);
+                                if (dres) cp_async16_part(to + z - off_s + off_d, gd + q, n > 16 ? 16 : n > 0 ? n : 0);
+                            }
+                            continue;
+                        }
+                    }
                     cp_async16(to + o, gy + o);
 #pragma unroll
                     for (int h = 0; h < VE * Io<R>::kBytes / 16; ++h) {
@@ -338,9 +451,12 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
         }
         cp_async_commit();
     };
+    if constexpr (SHIFT)
+        for (int c = threadIdx.x; c < Dp; c += blockDim.x)
+            if (c < m || c >= p.D + m) weight[c] = 0.0f;
     for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-        if (p.weight) cp_async4(weight + c, p.weight + c);
-        else weight[c] = 1.0f;
+        if (p.weight) cp_async4(weight + m + c, p.weight + c);
+        else weight[m + c] = 1.0f;
     }
     cp_async_commit();
 #pragma unroll
@@ -367,6 +483,18 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
             load_pairs<R, VE, NV>(STAGED ? nullptr : static_cast<const R *>(p.s) + row * p.D, from + off_s, at, z);
             load_pairs<IO, VE, NV>(STAGED ? nullptr : static_cast<const IO *>(p.dy) + row * p.D, from, at, v);
             load_pairs<float, VE, NV>(nullptr, smem_u32(weight), at, wt);
+            if constexpr (SHIFT) {  // other rows' values, which may be anything
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (edge(i)) {
+#pragma unroll
+                        for (int e = 0; e < VE; e += 2) {
+                            const int k = (i * VE + e) / 2;
+                            z[k] = and2(z[k], inside(i, e), inside(i, e + 1));
+                            v[k] = and2(v[k], inside(i, e), inside(i, e + 1));
+                        }
+                    }
+            }
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 if (VE > 1 && !live[2 * k / VE]) wt[k] = 0;
@@ -412,13 +540,22 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
                     o[e] = (i * VE + e) & 1 ? up : lo;
                 }
                 if (!live[i]) continue;
+                if (edge(i)) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        if (!inside(i, e)) continue;
+                        Io<R>::st(static_cast<R *>(p.ds) + row * p.D - m + at[i] + e, o[e]);
+                        if (p.dx) Io<IO>::st(static_cast<IO *>(p.dx) + row * p.D - m + at[i] + e, o[e]);
+                    }
+                    continue;
+                }
                 Raw<R, VE> q;
                 q.set(o);
-                q.store(static_cast<R *>(p.ds) + row * p.D + at[i]);
+                q.store(static_cast<R *>(p.ds) + row * p.D - m + at[i]);
                 if (p.dx) {
                     Raw<IO, VE> u;
                     u.set(o);
-                    u.store(static_cast<IO *>(p.dx) + row * p.D + at[i]);
+                    u.store(static_cast<IO *>(p.dx) + row * p.D - m + at[i]);
                 }
             }
         }
@@ -440,7 +577,7 @@ __global__ void __launch_bounds__(G ? 256 : kBwdThreads) norm_backward_kernel(co
                 const int c = (i * VE + e) / 2;
                 float lo, up;
                 unpack2(k == 0 ? dw[c] : db[c], lo, up);
-                if (live[i]) own[at[i] + e] = (i * VE + e) & 1 ? up : lo;
+                if (live[i] && (!SHIFT || inside(i, e))) own[at[i] + e - m] = (i * VE + e) & 1 ? up : lo;
             }
         }
         if constexpr (G) {

@@ -26,28 +26,32 @@ int check_sizes(int64_t rows, int64_t D, int dtype, uint32_t flags) {
 }
 
 // How a row is shared out: NV vectors of `ve` values a thread, `threads` threads a row (up
-// to 32: groups of lanes; more: a block a row), or nv = 0: too long for registers.
+// to 32: groups of lanes; more: a block a row), or nv = 0: too long for registers.  Rows of a
+// width that is not a multiple of 16 bytes: `shift`, by the aligned vectors that cover them
+// (4000 x 6001 bf16 with a residual, forward, 70 us; value by value 147), or value by value
+// where one warp takes a row.
 struct RowShape {
     int ve, nv, threads;
+    bool shift = false;
 };
+int64_t row_vectors(int64_t D, int ve, bool shift) { return shift ? ceil_div(D + ve - 1, ve) : D / ve; }
 RowShape row_shape(int64_t D, int es) {
-    const int ve = D * es % 16 == 0 ? 16 / es : 1;
-    const int64_t n = D / ve;
-    if (ve == 1) {  // single values: 8 a thread
-        if (n <= 256) return {1, 8, 32};
-        if (n <= 8 * norm::kMaxThreads) return {1, 8, static_cast<int>(ceil_div(n, 256) * 32)};
-        return {1, 0, 0};
+    const int ve = 16 / es;
+    const bool shift = D * es % 16 != 0;
+    if (shift && D <= 256) return {1, 8, 32};
+    const int64_t n = row_vectors(D, ve, shift);
+    if (!shift) {
+        if (n <= 8) return {ve, 1, 8};
+        if (n <= 16) return {ve, 1, 16};
+        if (n <= 32) return {ve, 1, 32};
+        if (n <= 64) return {ve, 2, 32};
+        if (n <= 128) return {ve, 4, 32};
+        if (es == 4 && n <= 256) return {ve, 8, 32};
     }
-    if (n <= 8) return {ve, 1, 8};
-    if (n <= 16) return {ve, 1, 16};
-    if (n <= 32) return {ve, 1, 32};
-    if (n <= 64) return {ve, 2, 32};
-    if (n <= 128) return {ve, 4, 32};
-    if (es == 4 && n <= 256) return {ve, 8, 32};
-    if (n <= 256) return {ve, 1, static_cast<int>(ceil_div(n, 32) * 32)};
-    if (n <= 1024) return {ve, 2, static_cast<int>(ceil_div(n, 64) * 32)};
-    if (n <= 4 * norm::kMaxThreads) return {ve, 4, static_cast<int>(ceil_div(n, 128) * 32)};
-    return {ve, 0, 0};
+    if (n <= 256) return {ve, 1, static_cast<int>(ceil_div(n, 32) * 32), shift};
+    if (n <= 1024) return {ve, 2, static_cast<int>(ceil_div(n, 64) * 32), shift};
+    if (n <= 4 * norm::kMaxThreads) return {ve, 4, static_cast<int>(ceil_div(n, 128) * 32), shift};
+    return {shift ? 1 : ve, 0, 0};
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
@@ -57,7 +61,7 @@ template <int ES, class F>
 int with_shape(const RowShape &sh, F f) {
     constexpr int V = 16 / ES;
     const bool group = sh.threads <= 32;
-    if (sh.ve == 1) return group ? f(Int<1>{}, Int<8>{}, Int<32>{}) : f(Int<1>{}, Int<8>{}, Int<0>{});
+    if (sh.ve == 1) return f(Int<1>{}, Int<8>{}, Int<32>{});
     if (sh.threads == 8) return f(Int<V>{}, Int<1>{}, Int<8>{});
     if (sh.threads == 16) return f(Int<V>{}, Int<1>{}, Int<16>{});
     if (sh.nv == 1) return group ? f(Int<V>{}, Int<1>{}, Int<32>{}) : f(Int<V>{}, Int<1>{}, Int<0>{});
@@ -76,8 +80,14 @@ int launch_forward(const norm::FwdParams &p, cudaStream_t s) {
     } else {
         with_shape<sizeof(IO)>(sh, [&](auto ve, auto nv, auto g) {
             constexpr int rows = g ? 128 / (g ? g : 1) : 1;  // of a block
-            norm::norm_forward_kernel<IO, R, RES, ve, nv, g>
-                <<<static_cast<unsigned>(ceil_div(p.rows, rows)), rows * sh.threads, 0, s>>>(p);
+            const unsigned blocks = static_cast<unsigned>(ceil_div(p.rows, rows));
+            if constexpr (!g) {
+                if (sh.shift) {
+                    norm::norm_forward_kernel<IO, R, RES, ve, nv, g, true><<<blocks, sh.threads, 0, s>>>(p);
+                    return 0;
+                }
+            }
+            norm::norm_forward_kernel<IO, R, RES, ve, nv, g, false><<<blocks, rows * sh.threads, 0, s>>>(p);
             return 0;
         });
     }
@@ -96,21 +106,18 @@ int64_t bwd_smem(int64_t D, int ve, bool dres, int rows, int stages) {
 }
 template <class IO, class R>
 RowShape bwd_row_shape(int64_t D, bool dres) {
-    RowShape sh = row_shape(D, sizeof(IO));
-    const int64_t n = D / sh.ve, smem = bwd_smem<IO, R>(D, sh.ve, dres, 1, norm::kBlockStages);
-    if (sh.ve == 1) {
-        if (n > 8 * norm::kBwdThreads) sh.nv = 0;
-        return sh;
-    }
+    const RowShape sh = row_shape(D, sizeof(IO));
+    if (sh.ve == 1 || sh.nv == 0) return sh;
+    const int64_t n = row_vectors(D, sh.ve, sh.shift), smem = bwd_smem<IO, R>(n * sh.ve, sh.ve, dres, 1, norm::kBlockStages);
     const int most = 16 / sh.ve;  // vectors a thread
-    if (bwd_smem<IO, R>(D, sh.ve, dres, 1, norm::kLongStages) > kRingBytes || n > int64_t(most) * norm::kBwdThreads)
-        return {sh.ve, 0, 0};
+    if (bwd_smem<IO, R>(n * sh.ve, sh.ve, dres, 1, norm::kLongStages) > kRingBytes || n > int64_t(most) * norm::kBwdThreads)
+        return {sh.shift ? 1 : sh.ve, 0, 0};
     if (sh.threads <= 32 && sh.nv <= most) return sh;
     // as few values a thread as leaves the SM's threads to as many rows as its shared memory holds
     const int64_t want = norm::kBwdThreads / (smem * 2 > kRingBytes ? 1 : smem * 4 > kRingBytes ? 2 : 4);
     int nv = 1;
     while (nv < most && n > want * nv) nv *= 2;
-    return {sh.ve, nv, static_cast<int>(ceil_div(n, 32 * nv) * 32)};
+    return {sh.ve, nv, static_cast<int>(ceil_div(n, 32 * nv) * 32), sh.shift};
 }
 
 // Backward blocks, each leaving one row of partial sums per gradient.
@@ -138,19 +145,26 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
             } else {
                 const bool dres = p.dresidual != nullptr;
                 const int threads = g ? kBwdGroupThreads : sh.threads;
-                auto launch = [&](auto stages) -> int {
-                    constexpr auto kern = norm::norm_backward_kernel<IO, R, ve, nv, g, stages>;
-                    const int64_t smem = bwd_smem<IO, R>(p.D, ve, dres, block_rows, stages);
+                const int64_t width = ve > 1 ? row_vectors(p.D, ve, sh.shift) * ve : p.D;
+                auto launch_as = [&](auto stages, auto shift) -> int {
+                    constexpr auto kern = norm::norm_backward_kernel<IO, R, ve, nv, g, stages, shift>;
+                    const int64_t smem = bwd_smem<IO, R>(width, ve, dres, block_rows, stages);
                     int per_sm = static_cast<int>((kRingBytes + 7 * 1024) / (smem + 1024));  // blocks of an SM
                     if (per_sm * threads > norm::kBwdThreads) per_sm = norm::kBwdThreads / threads;
                     at_most(148 * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm));
+                    if (shift && blocks < p.rows) blocks -= blocks % ve;  // a block's rows begin alike
                     if (smem_opt_in<kern>(static_cast<int>(kRingBytes)) != cudaSuccess) return SSCAN_ERR_CUDA;
                     kern<<<static_cast<unsigned>(blocks), threads, smem, s>>>(p);
                     return SSCAN_OK;
                 };
+                auto launch = [&](auto stages) -> int {
+                    if constexpr (!g)
+                        if (sh.shift) return launch_as(stages, Int<1>{});
+                    return launch_as(stages, Int<0>{});
+                };
                 if constexpr (g) return launch(Int<norm::kGroupStages>{});
                 if constexpr (ve > 1 && ve * nv == 16)  // rows that fill shared memory take 16 values a thread
-                    if (bwd_smem<IO, R>(p.D, ve, dres, 1, norm::kBlockStages) > kRingBytes)
+                    if (bwd_smem<IO, R>(width, ve, dres, 1, norm::kBlockStages) > kRingBytes)
                         return launch(Int<norm::kLongStages>{});
                 return launch(Int<norm::kBlockStages>{});
             }

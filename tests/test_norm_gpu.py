@@ -147,6 +147,26 @@ def test_rows_in_several_passes(rows, D, dtype, residual):
     check(rows, D, dtype, residual, False)
 
 
+@pytest.mark.parametrize("D", [257, 258, 301, 777, 2050, 4100, 5121])
+@pytest.mark.parametrize("dtype,residual", [("bf16", None), ("bf16", "f32"), ("bf16", "same"), ("f32", "same")])
+def test_rows_off_the_boundary(D, dtype, residual):
+    """Rows that begin inside a vector, for blocks of one row and of several; the rows next to a
+    bad one, which share its first and last vectors, are the same without it."""
+    check(1203 if D < 1000 else 800, D, dtype, residual, D % 3 == 0, bias=D % 2 == 0)
+    d = {k: None if v is None else v.cuda() for k, v in make(700, D, dtype, residual).items()}
+    run = lambda x, r, dy: (lambda f: (f, S.norm_backward(dy, f[1], f[2], f[3], d["weight"], d["dresidual"], want_dbias=True)))(
+        S.norm_forward(x, d["weight"], d["bias"], residual=r))
+    f, b = run(d["x"], d["residual"], d["dy"])
+    bad = [0, 5, 342, 343, 699]
+    x, dy = d["x"].clone(), d["dy"].clone()
+    x[bad] = float("nan")
+    dy[bad] = float("inf")
+    f2, b2 = run(x, d["residual"], dy)
+    keep = [i for i in range(700) if i not in bad]
+    for p, q in zip(f + (b["dx"], b["dresidual"]), f2 + (b2["dx"], b2["dresidual"])):
+        assert torch.equal(p[keep], q[keep])
+
+
 @pytest.mark.parametrize("mean", [0.0, 30.0, 1000.0])
 def test_a_mean_far_from_zero(mean):
     check(6, 640, "f32", None, False, mean=mean)

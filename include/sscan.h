@@ -285,9 +285,10 @@ SSCAN_API int sscan_ssd_forward(int64_t B, int64_t L, int64_t H, int64_t P, int6
  *   dtype              SSCAN_F32 or SSCAN_BF16: x, the gates and y
  *   x, gate            [B][L][D]
  *   input_gate         [B][L][D], or NULL
- *   rate               [D] fp32, every value > 0, or NULL.  Values above 80 (a decay of
- *                      2e-35 at s = 1) act as 80.  (A rate of 0 holds the state; its
- *                      gradient is not defined.)
+ *   rate               [D] fp32, every value > 0, or NULL.  Values above 2^21, infinity
+ *                      among them, act as 2^21 (no difference but for gates below -9.9).
+ *                      Decays below 2^-126 are 2^-126 to within a factor of sqrt(2).  (A
+ *                      rate of 0 holds the state; its gradient is not defined.)
  *   h0                 [B][D] fp32, or NULL for a zero initial state
  *   y                  [B][L][D] (output)
  *   h_final            [B][D] fp32 (output), or NULL; may be the same buffer as h0

@@ -63,14 +63,16 @@ __device__ __forceinline__ void sigmoid2(f2 g, f2 &s, f2 &n) {
 // a - v on the FMA pipe (flipping the sign bits would be two integer operations)
 __device__ __forceinline__ f2 minus2(f2 a, f2 v) { return fma2(v, splat2(-1.0f), a); }
 
-// The rate times log2 e of two channels.  Rates above 80 act as 80 (a decay of 2e-35 at
-// s = 1): z stays in the range of the exponent arithmetic below without a test per token.
-constexpr float kMaxRate = 80.0f;
+// Rates above 2^21, infinity among them, act as 2^21: e below stays under 2^22, where its
+// rounding is exact.  At every gate above -9.9 they decay by less than 2^-126 either way.
+constexpr float kMaxRate = 2097152.0f;
 __device__ __forceinline__ f2 capped_rate(f2 c) {
     return map2(c, [](float v) { return min_nan(v, kMaxRate); });
 }
 
-// a = e^-z and m = 1 - a, z = s c, from s in [0, 1] and cl = c log2 e.
+// a = e^-z and m = 1 - a, z = s c, from s in [0, 1] and cl = c log2 e.  j is held at 126, so that
+// decays below 2^-126 are about 2^-126.  (Held in t, which only S waits for: 1 x 131072 x 2048
+// bf16 606 us, without a hold 602; held in e, which f waits for too, 632.)
 // 2^-f - 1 = f q(f), with -q(-f) = ln 2 times the degree-5 minimax polynomial of (e^z - 1)/z
 // on |f| <= 1/2 (csrc/gen_phi_poly.py 5 0.3465735902799726 --log2: 1.1e-8, 1.4e-7 evaluated
 // in fp32).
@@ -85,7 +87,7 @@ __device__ __forceinline__ void decay2(f2 s, f2 cl, f2 &a, f2 &m) {
     q = fma2(q, f, splat2(-6.9314718246459961e-01f));
     const f2 p = mul2(q, f);
     float t0, t1;
-    unpack2(t, t0, t1);
+    unpack2(map2(t, [](float v) { return min_nan(v, 12582912.0f + 126.0f); }), t0, t1);
     const f2 S = pack2(__uint_as_float(__float_as_uint(t0) * 0xff800000u + 0x3f800000u),  // 2^-j
                        __uint_as_float(__float_as_uint(t1) * 0xff800000u + 0x3f800000u));
     a = fma2(S, p, S);

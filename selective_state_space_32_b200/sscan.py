@@ -428,7 +428,7 @@ def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=No
     """Gated linear recurrence (``sscan_glr_forward``) on CUDA tensors.
 
     x, gate and input_gate (or None): [B, L, D] float32 or bfloat16; rate: [D] float32 > 0
-    (above 80: as 80) or None; h0: [B, D] float32 or None.  h_final may be h0 (a decode step in place).
+    (above 2^21: as 2^21) or None; h0: [B, D] float32 or None.  h_final may be h0 (a decode step in place).
     ``want_states`` returns the saved states that ``glr_backward`` reads (or pass a buffer
     of ``new_glr_states`` as ``states``).  Work and new tensors are on ``stream`` (default:
     the current stream of x's device).

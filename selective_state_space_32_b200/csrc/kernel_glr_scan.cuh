@@ -230,8 +230,8 @@ __device__ __forceinline__ void send_map(float2 *local, uint64_t *bar, uint32_t 
                  : "memory");
 }
 // mbar_wait for bytes that other blocks of the cluster stored
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint32_t tries) {
+    for (uint32_t i = 0; i < tries; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -255,20 +255,23 @@ struct Shared {
     uint64_t *bar;
     uint32_t C, rank;
     int warps, w, lane;
-    // A wait for the cluster's maps gave up: the state is NaN from there on, and this thread
-    // sends and arms no more, so that the other blocks' waits give up too, once each.
-    bool lost;
+    Waits waits;
+    // A wait for the cluster's maps gave up (1 + the step's low two bits): the state is NaN from
+    // there on, and this thread sends and arms no more, so that the other blocks' waits give up
+    // too, once each.
+    int lost;
 
     // reads: have_read will follow
     __device__ __forceinline__ void init(unsigned char *smem, unsigned char *maps, int ch, uint32_t cluster,
-                                         bool reads = false) {
+                                         const Waits &wt, bool reads = false) {
         C = cluster;
+        waits = wt;
         rank = C > 1 ? cluster_rank() : 0;
         lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
         bar = reinterpret_cast<uint64_t *>(smem);
         agg = reinterpret_cast<float2 *>(maps);
         cl = agg + 2 * warps * ch;
-        lost = false;
+        lost = 0;
         if (C > 1) {
             if (threadIdx.x == 0) {
                 for (int k = 0; k < 2; ++k) mbar_init(bar + k, 1), mbar_expect_tx(bar + k, C * ch * 8);
@@ -288,10 +291,19 @@ struct Shared {
         __syncwarp();
         if (C > 1) cluster_wait();
     }
-    // A thread that lost a wait stays until the others have come here or ended: till then they
-    // may still send to its block.
+    // The wait of step `it` gave up (finish reports it: an atomic here instead, in the walk's
+    // loop, made the directly loaded bf16 backward 6 % slower).
+    __device__ __forceinline__ void give_up(int64_t it) { lost = 1 + static_cast<int>(it & 3); }
+    // A thread that lost a wait stays until what the others had sent for that step has arrived
+    // (for a bounded time: they may not have), and until they have come here or ended: till then
+    // they may still send to its block.  What a block sends later than that step, it sends
+    // before a wait of its own that gives up.
     __device__ __forceinline__ void finish() const {
-        if (lost) asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+        if (lost) {
+            if (waits.status) atomicOr(waits.status, kGaveUp);
+            mbar_wait_sleep(bar + (lost - 1 & 1), static_cast<uint32_t>(lost - 1 >> 1));
+            asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+        }
     }
 };
 
@@ -353,8 +365,8 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
         for (uint32_t r = w; r < sh.C; r += warps)
             send_map(sh.cl + (par * sh.C + sh.rank) * CH + sh.lane * V, sh.bar + par, r, Ab, Hb);
     }
-    if (!sh.lost && !mbar_wait_cluster(sh.bar + par, static_cast<uint32_t>(it >> 1) & 1)) {
-        sh.lost = true;
+    if (!sh.lost && !mbar_wait_cluster(sh.bar + par, static_cast<uint32_t>(it >> 1) & 1, sh.waits.tries)) {
+        sh.give_up(it);
         carry = LV::splat(__uint_as_float(0x7fc00000u));
     }
     if (threadIdx.x == 0 && !sh.lost) mbar_expect_tx(sh.bar + par, sh.C * CH * 8);  // for the second next step
@@ -383,7 +395,7 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
     const bool in_place = p.h0 && p.h_final == p.h0;
-    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, in_place);
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, p.waits, in_place);
     const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;
@@ -468,7 +480,7 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
-    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C);
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, p.waits);
     const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;

@@ -28,7 +28,8 @@ SYMBOLS = ("sscan_plan_create", "sscan_plan_destroy", "sscan_workspace_bytes", "
            "sscan_forward_noalloc", "sscan_noalloc_status", "sscan_forward_gated", "sscan_backward",
            "sscan_backward_workspace_bytes", "sscan_ssd_forward", "sscan_backward_gated",
            "sscan_host_workspace_bytes", "sscan_forward_host", "sscan_glr_states_bytes", "sscan_glr_forward",
-           "sscan_glr_backward_workspace_bytes", "sscan_glr_backward", "sscan_norm_forward",
+           "sscan_glr_forward_checked", "sscan_glr_backward_workspace_bytes", "sscan_glr_backward",
+           "sscan_glr_backward_checked", "sscan_norm_forward",
            "sscan_norm_backward_workspace_bytes", "sscan_norm_backward")
 
 
@@ -91,10 +92,14 @@ def lib() -> ctypes.CDLL:
             L.sscan_glr_states_bytes.restype = sz
             L.sscan_glr_forward.argtypes = [i64, i64, i64, ip] + [vp] * 9
             L.sscan_glr_forward.restype = ip
+            L.sscan_glr_forward_checked.argtypes = [i64, i64, i64, ip] + [vp] * 9 + [u32, vp]
+            L.sscan_glr_forward_checked.restype = ip
             L.sscan_glr_backward_workspace_bytes.argtypes = [i64, i64, i64]
             L.sscan_glr_backward_workspace_bytes.restype = sz
             L.sscan_glr_backward.argtypes = [i64, i64, i64, ip] + [vp] * 14
             L.sscan_glr_backward.restype = ip
+            L.sscan_glr_backward_checked.argtypes = [i64, i64, i64, ip] + [vp] * 14 + [u32, vp]
+            L.sscan_glr_backward_checked.restype = ip
             L.sscan_norm_forward.argtypes = [i64, i64, ip, u32, ctypes.c_float] + [vp] * 9
             L.sscan_norm_forward.restype = ip
             L.sscan_norm_backward_workspace_bytes.argtypes = [i64, i64]
@@ -423,24 +428,34 @@ def new_glr_states(B: int, L: int, D: int, device="cuda") -> torch.Tensor:
     return torch.empty(_glr_sizes(B, L, D)[0], dtype=_F32, device=device)
 
 
+_ALL_TRIES = 2 ** 32 - 1  # the library's own limit of a wait
+
+
+def _check_status(status, d):
+    if status.shape != (1,) or status.dtype != torch.int32 or status.get_device() != d:
+        raise _unlike("status", status, (1,), torch.int32, d)
+
+
 def glr_forward(x, gate, rate=None, input_gate=None, h0=None, y=None, h_final=None, want_final: bool = True,
-                states=None, want_states: bool = False, stream=None):
+                states=None, want_states: bool = False, stream=None, status=None):
     """Gated linear recurrence (``sscan_glr_forward``) on CUDA tensors.
 
     x, gate and input_gate (or None): [B, L, D] float32 or bfloat16; rate: [D] float32 > 0
     (above 2^21: as 2^21) or None; h0: [B, D] float32 or None.  h_final may be h0 (a decode step in place).
     ``want_states`` returns the saved states that ``glr_backward`` reads (or pass a buffer
     of ``new_glr_states`` as ``states``).  Work and new tensors are on ``stream`` (default:
-    the current stream of x's device).
+    the current stream of x's device).  ``status``: a CUDA int32 tensor of one element, set to
+    non-zero when a wait inside the kernel gives up (outputs then hold NaN), or None.
     Returns (y [B, L, D], h_final [B, D] float32 or None, states or None)."""
     d = x.get_device()
     if stream is None and d >= 0 and d == _device_now():
-        return _glr_forward(_raw_stream(d), x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states)
+        return _glr_forward(_raw_stream(d), x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states,
+                            status)
     return _elsewhere(_glr_forward, x, stream,
-                      (x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states))
+                      (x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states, status))
 
 
-def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states):
+def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, states, want_states, status):
     shape, dt, d = x.shape, x.dtype, x.get_device()
     code = _CODES.get(dt)
     if code is None:
@@ -478,29 +493,38 @@ def _glr_forward(st, x, gate, rate, input_gate, h0, y, h_final, want_final, stat
             raise _unlike("states", states, (_glr_sizes(B, L, D)[0],), _F32, d)
     elif want_states:
         states = x.new_empty(_glr_sizes(B, L, D)[0], dtype=_F32)
-    rc = (_lib or lib()).sscan_glr_forward(
-        B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0), y.data_ptr(),
-        _adr(h_final), _adr(states), st)
+    if status is None:
+        rc = (_lib or lib()).sscan_glr_forward(
+            B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0), y.data_ptr(),
+            _adr(h_final), _adr(states), st)
+    else:
+        _check_status(status, d)
+        rc = (_lib or lib()).sscan_glr_forward_checked(
+            B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), _adr(h0), y.data_ptr(),
+            _adr(h_final), _adr(states), status.data_ptr(), _ALL_TRIES, st)
     if rc != OK:
         raise SscanError(rc, "sscan_glr_forward")
     return y, h_final, states
 
 
 def glr_backward(x, gate, dy, states, rate=None, input_gate=None, dh_final=None, want_dh0: bool = True,
-                 workspace=None, stream=None) -> dict:
+                 workspace=None, stream=None, status=None) -> dict:
     """Gradients of ``glr_forward`` (``sscan_glr_backward``): x, gate, rate and input_gate as
     passed to it, ``states`` as it returned them, dy [B, L, D] and dh_final [B, D] float32
     (or None).  Returns a dict with dx, dgate and dinput_gate (dtype of x; the last None
     without an input gate), drate ([D] float32, None without a rate) and dh0 ([B, D]
     float32, None unless wanted).  ``workspace``: a CUDA uint8 tensor of at least
-    ``sscan_glr_backward_workspace_bytes`` (default: allocated here)."""
+    ``sscan_glr_backward_workspace_bytes`` (default: allocated here).  ``status`` as for
+    ``glr_forward``."""
     d = x.get_device()
     if stream is None and d >= 0 and d == _device_now():
-        return _glr_backward(_raw_stream(d), x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace)
-    return _elsewhere(_glr_backward, x, stream, (x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace))
+        return _glr_backward(_raw_stream(d), x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace,
+                             status)
+    return _elsewhere(_glr_backward, x, stream,
+                      (x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace, status))
 
 
-def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace):
+def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0, workspace, status):
     shape, dt, d = x.shape, x.dtype, x.get_device()
     code = _CODES.get(dt)
     if code is None:
@@ -537,9 +561,16 @@ def _glr_backward(st, x, gate, dy, states, rate, input_gate, dh_final, want_dh0,
     else:
         workspace = None
     dx, dgate = torch.empty_like(x), torch.empty_like(x)
-    rc = (_lib or lib()).sscan_glr_backward(
-        B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), states.data_ptr(), dy.data_ptr(),
-        _adr(dh_final), dx.data_ptr(), dgate.data_ptr(), _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
+    if status is None:
+        rc = (_lib or lib()).sscan_glr_backward(
+            B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), states.data_ptr(), dy.data_ptr(),
+            _adr(dh_final), dx.data_ptr(), dgate.data_ptr(), _adr(dig), _adr(drate), _adr(dh0), _adr(workspace), st)
+    else:
+        _check_status(status, d)
+        rc = (_lib or lib()).sscan_glr_backward_checked(
+            B, L, D, code, x.data_ptr(), gate.data_ptr(), _adr(input_gate), _adr(rate), states.data_ptr(), dy.data_ptr(),
+            _adr(dh_final), dx.data_ptr(), dgate.data_ptr(), _adr(dig), _adr(drate), _adr(dh0), _adr(workspace),
+            status.data_ptr(), _ALL_TRIES, st)
     if rc != OK:
         raise SscanError(rc, "sscan_glr_backward")
     return {"dx": dx, "dgate": dgate, "dinput_gate": dig, "drate": drate, "dh0": dh0}

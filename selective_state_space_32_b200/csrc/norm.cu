@@ -66,7 +66,8 @@ int with_shape(const RowShape &sh, F f) {
     if (sh.threads == 16) return f(Int<V>{}, Int<1>{}, Int<16>{});
     if (sh.nv == 1) return group ? f(Int<V>{}, Int<1>{}, Int<32>{}) : f(Int<V>{}, Int<1>{}, Int<0>{});
     if (sh.nv == 2) return group ? f(Int<V>{}, Int<2>{}, Int<32>{}) : f(Int<V>{}, Int<2>{}, Int<0>{});
-    if (ES == 4 && sh.nv == 8) return f(Int<V>{}, Int<8>{}, Int<32>{});
+    if constexpr (ES == 4)
+        if (sh.nv == 8) return f(Int<V>{}, Int<8>{}, Int<32>{});
     return group ? f(Int<V>{}, Int<4>{}, Int<32>{}) : f(Int<V>{}, Int<4>{}, Int<0>{});
 }
 
@@ -87,7 +88,8 @@ int launch_forward(const norm::FwdParams &p, cudaStream_t s) {
                     return 0;
                 }
             }
-            norm::norm_forward_kernel<IO, R, RES, ve, nv, g, false><<<blocks, rows * sh.threads, 0, s>>>(p);
+            if constexpr (g || nv > 1 || sizeof(IO) == 2)  // aligned fp32 rows of 256 vectors are a warp's
+                norm::norm_forward_kernel<IO, R, RES, ve, nv, g, false><<<blocks, rows * sh.threads, 0, s>>>(p);
             return 0;
         });
     }
@@ -162,11 +164,18 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
                         if (sh.shift) return launch_as(stages, Int<1>{});
                     return launch_as(stages, Int<0>{});
                 };
-                if constexpr (g) return launch(Int<norm::kGroupStages>{});
-                if constexpr (ve > 1 && ve * nv == 16)  // rows that fill shared memory take 16 values a thread
-                    if (bwd_smem<IO, R>(width, ve, dres, 1, norm::kBlockStages) > kRingBytes)
-                        return launch(Int<norm::kLongStages>{});
-                return launch(Int<norm::kBlockStages>{});
+                // rows that fill shared memory take 16 values a thread, and some types' never do
+                constexpr int64_t widest = 16 * norm::kBwdThreads;
+                constexpr bool fills = ve > 1 && ve * nv == 16 &&
+                                       widest * 4 + norm::kBlockStages * norm::bwd_row_bytes<IO, R>(widest, true) > kRingBytes;
+                if constexpr (g) {
+                    return launch(Int<norm::kGroupStages>{});
+                } else {
+                    if constexpr (fills)
+                        if (bwd_smem<IO, R>(width, ve, dres, 1, norm::kBlockStages) > kRingBytes)
+                            return launch(Int<norm::kLongStages>{});
+                    return launch(Int<norm::kBlockStages>{});
+                }
             }
         });
     }

@@ -379,8 +379,9 @@ def ssd_forward(x, delta, A, B, C, h0=None, y=None, h_final=None, want_final: bo
 
 _F32 = torch.float32
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_device_now = getattr(torch._C, "_cuda_getDevice", None)
+# torch's quicker names for these are private: the public ones where it lacks them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _unlike(name, t, shape, dt, d):

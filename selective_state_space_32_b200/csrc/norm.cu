@@ -122,8 +122,16 @@ RowShape bwd_row_shape(int64_t D, bool dres) {
     return {sh.ve, nv, static_cast<int>(ceil_div(n, 32 * nv) * 32), sh.shift};
 }
 
-// Backward blocks, each leaving one row of partial sums per gradient.
-constexpr int64_t kMaxBwdBlocks = 148 * 4;
+// Backward blocks, each leaving one row of partial sums per gradient; where a row takes several
+// passes, so many that the rows a block reads twice stay in the L2.
+constexpr int64_t kMaxBwdBlocks = 148 * 4, kLongBwdBlocks = 148;
+int64_t most_bwd_blocks(int64_t D) {  // of any types
+    for (bool dres : {false, true})
+        if (bwd_row_shape<float, float>(D, dres).nv || bwd_row_shape<uint16_t, uint16_t>(D, dres).nv ||
+            bwd_row_shape<uint16_t, float>(D, dres).nv)
+            return kMaxBwdBlocks;
+    return kLongBwdBlocks;
+}
 constexpr int kBwdGroupThreads = 256;  // of a block of several rows
 
 template <class IO, class R>
@@ -134,7 +142,7 @@ int launch_backward(const norm::BwdParams &p, float *dweight, float *dbias, cuda
     int rc = SSCAN_OK;
     auto at_most = [&](int64_t n) { blocks = blocks < n ? blocks : n; };
     if (sh.nv == 0) {
-        at_most(148);  // the rows that a block reads twice stay in the L2
+        at_most(kLongBwdBlocks);
         const int64_t each = ceil_div(p.rows, blocks);
         blocks = ceil_div(p.rows, each);
         const unsigned n = static_cast<unsigned>(blocks);
@@ -218,7 +226,8 @@ int sscan_norm_forward(int64_t rows, int64_t D, int dtype, uint32_t flags, float
 
 size_t sscan_norm_backward_workspace_bytes(int64_t rows, int64_t D) {
     if (check_sizes(rows, D, SSCAN_F32, 0) != SSCAN_OK || rows == 0) return 0;
-    return round_up_256(2 * size_t(rows < kMaxBwdBlocks ? rows : kMaxBwdBlocks) * size_t(D) * sizeof(float));
+    const int64_t most = most_bwd_blocks(D);
+    return round_up_256(2 * size_t(rows < most ? rows : most) * size_t(D) * sizeof(float));
 }
 
 int sscan_norm_backward(int64_t rows, int64_t D, int dtype, uint32_t flags, const void *dy, const void *s_in,

@@ -92,3 +92,15 @@ def compiled():
 def test_the_library_holds_the_kernels_that_calls_reach():
     have, want = compiled(), forward_kernels() | backward_kernels()
     assert have == want, (sorted(map(str, have - want)), sorted(map(str, want - have)))
+
+
+def test_the_workspace_is_what_the_blocks_use():
+    """Two rows of D sums a block: 148 blocks where every type takes several passes over a row, else at most 592."""
+    from selective_state_space_32_b200 import sscan as S
+    B.build()
+    ws = S.lib().sscan_norm_backward_workspace_bytes
+    for D in (10241, 10248, 12288, WIDEST):
+        assert ws(3000, D) == up(2 * 148 * D * 4, 256) * 256
+        assert ws(5, D) == up(2 * 5 * D * 4, 256) * 256
+    for D in (64, 777, 5120, 10240):
+        assert ws(3000, D) == up(2 * 592 * D * 4, 256) * 256

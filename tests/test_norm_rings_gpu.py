@@ -49,3 +49,17 @@ def test_neighbours_of_bad_rows_and_the_same_bits(dtype, residual, D):
     for p, q in zip(f + (b["dx"], b["dresidual"]), f2 + (b2["dx"], b2["dresidual"])):
         assert torch.equal(p[keep], q[keep])
         assert not torch.isfinite(q[bad]).any()
+
+
+@pytest.mark.parametrize("rows,dtype,residual,D", [(700, "f32", "same", 10244), (700, "bf16", "f32", 12288), (3, "bf16", None, 40001),
+                                                   (601, "bf16", "same", 10240), (601, "f32", None, 777)])
+def test_the_workspace_is_as_large_as_stated(rows, dtype, residual, D):
+    """A workspace of just that size inside a larger buffer: the rest keeps its values, the gradients their bits."""
+    d = {k: None if v is None else v.cuda() for k, v in make(rows, D, dtype, residual).items()}
+    y, s, mu, rstd = S.norm_forward(d["x"], d["weight"], d["bias"], residual=d["residual"])
+    want = S.norm_backward(d["dy"], s, mu, rstd, d["weight"], d["dresidual"], want_dbias=True)
+    n = int(S.lib().sscan_norm_backward_workspace_bytes(rows, D))
+    big = torch.full((n + 8192,), 7, dtype=torch.uint8, device="cuda")
+    got = S.norm_backward(d["dy"], s, mu, rstd, d["weight"], d["dresidual"], want_dbias=True, workspace=big[4096:4096 + n])
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    assert (big[:4096] == 7).all() and (big[4096 + n:] == 7).all()

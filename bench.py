@@ -68,7 +68,7 @@ def strip_comments(src: str) -> str:
 SSD_SOURCES = ("kernel_ssd.cuh", "ssd.cu")
 HOST_ONLY_SOURCES = ("host_pipe.cu",)  # copies and sub-plan calls: no kernel launch of its own
 # the recurrent block's other operators, whose kernels no workload here launches
-BLOCK_SOURCES = ("abi_checks.cuh", "column_sums.cuh", "glr.cu", "glr_math.cuh", "kernel_glr.cuh",
+BLOCK_SOURCES = ("abi_checks.cuh", "column_sums.cuh", "cp_async.cuh", "glr.cu", "glr_math.cuh", "kernel_glr.cuh",
                  "kernel_glr_scan.cuh", "kernel_norm.cuh", "norm.cu")
 
 

@@ -37,6 +37,7 @@
 // time; STAGED = false loads them from memory, one channel a lane.
 #pragma once
 
+#include "cp_async.cuh"
 #include "device_utils.cuh"
 #include "glr_math.cuh"
 #include "kernel_glr.cuh"
@@ -75,16 +76,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zeros(void *dst, const void *src, bool on) {
-    const int n = on ? 16 : 0;  // 0: nothing is read, 16 zero bytes are written
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // The warp's index, known to the compiler to be the same in its lanes (row addresses are
 // then formed once a warp)
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
@@ -155,9 +146,9 @@ struct RunLoader {
                     for (int s = 0; s < NS; ++s)
 #pragma unroll
                         for (int h = 0; h < K / kRows; ++h)
-                            cp_async16_or_zeros(dst + (s * K + kRows * h) * kRowBytes,
-                                                row + kRows * h < n ? src[s] + off + h * next + own : src[s],
-                                                row + kRows * h < n);
+                            cp_async16_part(smem_u32(dst + (s * K + kRows * h) * kRowBytes),
+                                            row + kRows * h < n ? src[s] + off + h * next + own : src[s],
+                                            row + kRows * h < n ? 16 : 0);
                 }
             }
             cp_async_commit();

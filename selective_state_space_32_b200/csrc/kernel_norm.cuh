@@ -37,6 +37,7 @@
 // 5 of 35 instructions a value (16384 x 5120 142 us, 16384 x 768 50 us).
 #pragma once
 
+#include "cp_async.cuh"
 #include "device_utils.cuh"
 
 namespace sscan {
@@ -318,18 +319,6 @@ __global__ void __launch_bounds__(G ? 128 : kMaxThreads) norm_forward_kernel(con
         if (p.rstd) p.rstd[row] = rstd;
     }
 }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int bytes) {  // then zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Rows of a ring: a group's, a block's, and a block's whose rows are so long that shared
 // memory holds only one (4000 rows of 8192 fp32 values with a residual)

@@ -109,7 +109,7 @@ struct Launch {
 };
 
 template <class IO, int V, bool STAGED, bool DECAY, bool IG>
-int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
+int launch_scan(const glr::FwdParams &p, const glr::Waits &waits, cudaStream_t s) {
     constexpr int NS = IG ? 3 : 2, K = glr::kForwardRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
     const Shape sh = scan_shape(p.B * groups, ceil_div(p.L, K), forward_fill(STAGED));
@@ -117,12 +117,12 @@ int launch_scan(const glr::FwdParams &p, cudaStream_t s) {
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
     Launch l(p.B * groups * sh.cluster, sh, glr::scan_smem_bytes<IO, V, STAGED, NS, K>(sh.warps, sh.cluster), s);
-    return cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) == cudaSuccess ? SSCAN_OK
-                                                                                                       : SSCAN_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, p, waits, groups, static_cast<uint32_t>(sh.cluster));
+    return e == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
 }
 
 template <class IO, bool DECAY, bool IG>
-int launch_forward(const glr::FwdParams &p, cudaStream_t s) {
+int launch_forward(const glr::FwdParams &p, const glr::Waits &waits, cudaStream_t s) {
     if (p.L <= kStepTokens) {
         const bool pairs = p.D % 2 == 0;
         const unsigned blocks = static_cast<unsigned>(ceil_div(p.B * p.D, (pairs ? 2 : 1) * glr::kStepThreads));
@@ -132,12 +132,12 @@ int launch_forward(const glr::FwdParams &p, cudaStream_t s) {
             glr::glr_step_kernel<IO, 1, DECAY, IG><<<blocks, glr::kStepThreads, 0, s>>>(p);
         return cudaGetLastError() == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
     }
-    if (!staged<IO>(p.D)) return launch_scan<IO, 1, false, DECAY, IG>(p, s);
-    return launch_scan<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, s);
+    if (!staged<IO>(p.D)) return launch_scan<IO, 1, false, DECAY, IG>(p, waits, s);
+    return launch_scan<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, waits, s);
 }
 
 template <class IO, int V, bool STAGED, bool DECAY, bool IG>
-int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
+int launch_scan_backward(const glr::BwdParams &p, const glr::Waits &waits, float *drate, cudaStream_t s) {
     constexpr int NS = IG ? 4 : 3, K = glr::kRun;
     const int64_t groups = ceil_div(p.D, 32 * V);
     const Shape sh = scan_shape(p.B * groups, p.nruns, backward_fill(STAGED, glr::scan_blocks<V>()));
@@ -145,7 +145,8 @@ int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) 
     if (cluster_opt_in<kern>(glr::scan_smem_bytes<IO, V, STAGED, NS, K>(glr::kMaxWarps, glr::kMaxCluster)) != cudaSuccess)
         return SSCAN_ERR_CUDA;
     Launch l(p.B * groups * sh.cluster, sh, glr::scan_smem_bytes<IO, V, STAGED, NS, K>(sh.warps, sh.cluster), s);
-    if (cudaLaunchKernelEx(&l.cfg, kern, p, groups, static_cast<uint32_t>(sh.cluster)) != cudaSuccess) return SSCAN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&l.cfg, kern, p, waits, groups, static_cast<uint32_t>(sh.cluster)) != cudaSuccess)
+        return SSCAN_ERR_CUDA;
     if (!DECAY) return SSCAN_OK;
     const ColumnSums cs = {p.part, {drate, nullptr}, p.B * sh.cluster, p.D, 0};
     column_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(p.D, 32))), kColThreads, 0, s>>>(cs);
@@ -153,21 +154,24 @@ int launch_scan_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) 
 }
 
 template <class IO, bool DECAY, bool IG>
-int launch_backward(const glr::BwdParams &p, float *drate, cudaStream_t s) {
-    if (!staged<IO>(p.D)) return launch_scan_backward<IO, 1, false, DECAY, IG>(p, drate, s);
-    return launch_scan_backward<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, drate, s);
+int launch_backward(const glr::BwdParams &p, const glr::Waits &waits, float *drate, cudaStream_t s) {
+    if (!staged<IO>(p.D)) return launch_scan_backward<IO, 1, false, DECAY, IG>(p, waits, drate, s);
+    return launch_scan_backward<IO, glr::lane_channels<IO, true>(), true, DECAY, IG>(p, waits, drate, s);
 }
 
 template <class IO>
-int forward_t(const glr::FwdParams &p, cudaStream_t s) {
-    if (p.rate) return p.igate ? launch_forward<IO, true, true>(p, s) : launch_forward<IO, true, false>(p, s);
-    return p.igate ? launch_forward<IO, false, true>(p, s) : launch_forward<IO, false, false>(p, s);
+int forward_t(const glr::FwdParams &p, const glr::Waits &waits, cudaStream_t s) {
+    if (p.rate)
+        return p.igate ? launch_forward<IO, true, true>(p, waits, s) : launch_forward<IO, true, false>(p, waits, s);
+    return p.igate ? launch_forward<IO, false, true>(p, waits, s) : launch_forward<IO, false, false>(p, waits, s);
 }
 template <class IO>
-int backward_t(const glr::BwdParams &p, float *drate, cudaStream_t s) {
+int backward_t(const glr::BwdParams &p, const glr::Waits &waits, float *drate, cudaStream_t s) {
     if (p.rate)
-        return p.igate ? launch_backward<IO, true, true>(p, drate, s) : launch_backward<IO, true, false>(p, drate, s);
-    return p.igate ? launch_backward<IO, false, true>(p, drate, s) : launch_backward<IO, false, false>(p, drate, s);
+        return p.igate ? launch_backward<IO, true, true>(p, waits, drate, s)
+                       : launch_backward<IO, true, false>(p, waits, drate, s);
+    return p.igate ? launch_backward<IO, false, true>(p, waits, drate, s)
+                   : launch_backward<IO, false, false>(p, waits, drate, s);
 }
 
 size_t states_bytes(int64_t B, int64_t L, int64_t D) {
@@ -214,8 +218,8 @@ int forward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const voi
                                  : cudaMemsetAsync(h_final, 0, nh, s);
         return e == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
     }
-    const glr::FwdParams p = {x, gate, input_gate, rate, h0, y, h_final, states, B, L, D, runs(L), waits};
-    return dtype == SSCAN_F32 ? forward_t<float>(p, s) : forward_t<uint16_t>(p, s);
+    const glr::FwdParams p = {x, gate, input_gate, rate, h0, y, h_final, states, B, L, D, runs(L)};
+    return dtype == SSCAN_F32 ? forward_t<float>(p, waits, s) : forward_t<uint16_t>(p, waits, s);
 }
 
 size_t workspace_bytes(int64_t B, int64_t L, int64_t D) {
@@ -257,8 +261,8 @@ int backward(int64_t B, int64_t L, int64_t D, int dtype, const void *x, const vo
         return SSCAN_OK;
     }
     const glr::BwdParams p = {x, gate, input_gate, dy, rate, states, dh_final, dx, dgate, dinput_gate, dh0,
-                              static_cast<float *>(workspace), B, L, D, runs(L), waits};
-    return dtype == SSCAN_F32 ? backward_t<float>(p, drate, s) : backward_t<uint16_t>(p, drate, s);
+                              static_cast<float *>(workspace), B, L, D, runs(L)};
+    return dtype == SSCAN_F32 ? backward_t<float>(p, waits, drate, s) : backward_t<uint16_t>(p, waits, drate, s);
 }
 
 }  // namespace

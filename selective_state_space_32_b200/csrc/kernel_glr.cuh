@@ -18,21 +18,12 @@ namespace glr {
 
 constexpr int kRun = 8;  // tokens between two saved states
 
-// The waits of a cluster's blocks for one another: how often each looks before it gives up,
-// and the caller's word (or null) that is told of it.
-struct Waits {
-    int *status;
-    uint32_t tries;
-};
-constexpr int kGaveUp = 1;  // the bit set in *status
-
 struct FwdParams {
     const void *x, *gate, *igate;
     const float *rate, *h0;
     void *y;
     float *h_final, *states;
     int64_t B, L, D, nruns;
-    Waits waits;
 };
 
 struct BwdParams {
@@ -41,7 +32,6 @@ struct BwdParams {
     void *dx, *dgate, *digate;
     float *dh0, *part;  // part: partial sums of drate (with a rate), rows of D
     int64_t B, L, D, nruns;
-    Waits waits;
 };
 
 // V = 1 or 2 consecutive channels as a pair (V = 1: the second half repeats the first)

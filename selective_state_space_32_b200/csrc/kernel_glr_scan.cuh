@@ -236,6 +236,15 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     return false;
 }
 
+// The waits of a cluster's blocks for one another: how often each looks before it gives up,
+// and the caller's word (or null) that is told of it.  An argument of its own: as a part of
+// FwdParams it made the launch of the step kernel, which has no waits, 0.7 us longer.
+struct Waits {
+    int *status;
+    uint32_t tries;
+};
+constexpr int kGaveUp = 1;  // the bit set in *status
+
 // What the blocks and warps of a cluster share in a walk: agg [2][warps][CH] and
 // cl [2][C][CH] maps and two mbarriers, used in turn by the steps.  A step's entries are
 // overwritten two steps later: by then this block's warps have met at the step between
@@ -376,7 +385,7 @@ __device__ __forceinline__ typename Lane<V>::T exchange(typename Lane<V>::T A, t
 // grid: B * groups * C blocks of 32 W threads in clusters of C
 template <class IO, int V, bool STAGED, bool DECAY, bool IG, int K>
 __global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<V>())
-glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
+glr_scan_kernel(const FwdParams p, const Waits waits, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 3 : 2;
     using Loader = RunLoader<IO, V, STAGED, NS, K>;
     constexpr int CH = Loader::CH, NP = Loader::NP;
@@ -386,7 +395,7 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
     const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
     const bool in_place = p.h0 && p.h_final == p.h0;
-    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, p.waits, in_place);
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, waits, in_place);
     const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;
@@ -462,7 +471,7 @@ glr_scan_kernel(const FwdParams p, int64_t groups, uint32_t C) {
 // this block's channels.
 template <class IO, int V, bool STAGED, bool DECAY, bool IG>
 __global__ void __launch_bounds__(32 * kMaxWarps, scan_blocks<V>())
-glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
+glr_scan_backward_kernel(const BwdParams p, const Waits waits, int64_t groups, uint32_t C) {
     constexpr int NS = IG ? 4 : 3, K = kRun;
     using Loader = RunLoader<IO, V, STAGED, NS, K>;
     constexpr int CH = Loader::CH, NP = Loader::NP;
@@ -471,7 +480,7 @@ glr_scan_backward_kernel(const BwdParams p, int64_t groups, uint32_t C) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, w = warp_index(), warps = blockDim.x >> 5;
     Shared sh;
-    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, p.waits);
+    sh.init(smem, smem + 128 + (STAGED ? warps * kStages * Loader::kStageBytes : 0), CH, C, waits);
     const uint32_t rank = sh.rank;
     const int64_t cid = blockIdx.x / C, b = cid / groups, ch0 = (cid - b * groups) * CH;
     const int64_t row0 = b * p.L * p.D + ch0;

@@ -11,18 +11,22 @@
 //   3. every thread applies what precedes its run to the carried state, walks its
 //      tokens once more and stores them; the carried state moves on by the composition
 //      of the whole step, which every block forms for itself in the same order.
-// So x and the gates are read once, y is written once, nothing goes through a workspace,
-// no block waits on a flag, and the order of the sums depends on the sizes only.  The
-// next steps' inputs arrive by cp.async in a ring of each warp's own while this one runs.
+// So x and the gates are read once, y is written once, and the order of the sums depends on the
+// sizes only.  Only drate's partial sums go through a workspace.  The blocks of a cluster wait for
+// each other's maps on mbarriers in shared memory, for a bounded time; the blocks of different
+// clusters do not wait.  The next steps' inputs arrive by cp.async in a ring of each warp's own
+// while this one runs.
 // The backward pass is the same walk from the last token: G_t = dy_t + e, e <- a_t G_t is
 // a map of e, with the states of a run recomputed from the saved state before it.
 //
 // What bounds it (B200).  fp32 is a stream: 8 x 2048 x 1536 without a rate 49 us, 95 % of the
-// copy rate.  bf16 moves half the bytes and is held by instructions: with a rate and an input
-// gate 34 a value forward, of which 18 on the FMA pipe and 4 on the MUFU (52 us for
-// 8 x 2048 x 1536, 60 % of the copy rate; issue 52 % busy, MUFU 49 %, FMA 49 %), 68 backward
-// (104 us, 54 %); without them 73 and 154 us for 2 x 8192 x 4096 (85 and 71 %).  A few long
-// walks wait for their exchanges: 1 x 131072 x 2048 602 us (55 %).
+// copy rate.  bf16 moves half the bytes and waits: with a rate and an input gate 39 instructions
+// a value forward, of which 19 on the FMA pipe and 4 on the MUFU (52 us for 8 x 2048 x 1536,
+// 60 % of the copy rate), 70 backward (104 us, 54 %); issue is 58 and 52 % busy, no pipe above
+// 50 %, and the 9.6 warps of an SM spend their time on fixed latencies (0.9 of 2.1 and 1.0 of 2.8
+// stall cycles an instruction) and on memory and the cluster's maps (0.5 and 0.9).  Without rate
+// and input gate 72 and 154 us for 2 x 8192 x 4096 (86 and 71 %).  A few long walks wait for their
+// exchanges: 1 x 131072 x 2048 591 us (56 %).
 //
 // Runs of 16 tokens halve the exchanges of runs of 8 (67 against 74 us for the first bf16
 // case); the backward pass would not fit its registers with them.  Maps by st.async instead of

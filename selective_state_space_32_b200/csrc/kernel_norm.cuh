@@ -31,7 +31,9 @@
 // bf16 56 us, 74 %; 16384 x 768 bf16 39 us, 79 %).  Widths that are not a multiple of 16 bytes, by
 // the aligned vectors that cover a row: 4000 x 6001 bf16 with a residual 70 and 81 us (42 and
 // 37 %), 4000 x 7999 with an fp32 one 96 and 176, 8000 x 1999 41 and 49, 2001 x 777 fp32 8 and 12;
-// value by value 147 and 223, 166 and 322, 60 and 74, 7.5 and 12.5.
+// value by value 147 and 223, 166 and 322, 60 and 74, 7.5 and 12.5.  What holds them: forward 51 to
+// 63 registers against 32, so half the warps; backward with 16 values a thread 72 to 276 bytes of
+// registers spilled under the 96 that 640 threads leave.
 //
 // The rings are addressed by 32-bit shared addresses; as pointers, their 64-bit arithmetic was
 // 5 of 35 instructions a value (16384 x 5120 142 us, 16384 x 768 50 us).

@@ -375,7 +375,8 @@ def ssd_forward(x, delta, A, B, C, h0=None, y=None, h_final=None, want_final: bo
 # Recurrent block operators: the gated linear recurrence and the layer norm.  A decode
 # step runs in a few microseconds on the device, so these wrappers keep to what a call
 # needs: checks of attributes (written out: a function call each would cost as much as the
-# check), one allocation per output, the current stream's handle.
+# check), one allocation per output, the current stream's handle.  None of them records an
+# autograd graph: outputs never require a gradient, and the backward functions are called by hand.
 
 _F32 = torch.float32
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}

@@ -102,19 +102,21 @@ __device__ __forceinline__ void token2(f2 x, f2 g, f2 ig, f2 cl, f2 &a, f2 &b) {
         decay2(rcp2(one_plus_exp(g)), cl, a, m);
         const f2 r = minus2(splat2(2.0f), m), w = mul2(m, r);
         f2 v = fma2(m, r, splat2(kTiny));  // w = 0 (a = 1) gives beta = 0, not 0 * inf
-        // beta sigmoid(ig) = sqrt(w) / (1 + E) = w rsqrt(w (1 + E)^2): one MUFU operation for the
-        // square root and the quotient.  The square is of (1 + E) k in [2, 4), and x takes the
-        // k; a power of two, from the complement of 1 + E's exponent.  (Without k the square
-        // overflows for ig below -44; a reciprocal of its own: 1 x 131072 x 2048 bf16 632 us
-        // instead of 609, without either 607.)
+        // beta sigmoid(ig) = sqrt(w) / (1 + E) = w rsqrt(w q^2) k with q = (1 + E) k: one MUFU operation
+        // for the square root and the quotient.  k is the power of two, from the complement of
+        // 1 + E's exponent, that puts q in [2, 4).  (Without k the square overflows for ig below -44; a
+        // reciprocal of its own: 1 x 131072 x 2048 bf16 632 us instead of 602.  k into x, which
+        // overflows where x is above half the largest number: 591.)
+        f2 k = 0;
         if constexpr (IG) {
-            const f2 q = add2(map2(mul2(ig, splat2(-kLog2e)), [](float e) { return ex2(min_nan(e, 126.0f)); }), splat2(1.0f));
-            const f2 k = map2(q, [](float y) { return __uint_as_float(~__float_as_uint(y) & 0x7f800000u); });
-            const f2 qk = mul2(q, k);
-            v = mul2(v, mul2(qk, qk));
-            x = mul2(x, k);
+            f2 q = add2(map2(mul2(ig, splat2(-kLog2e)), [](float e) { return ex2(min_nan(e, 126.0f)); }), splat2(1.0f));
+            k = map2(q, [](float y) { return __uint_as_float(~__float_as_uint(y) & 0x7f800000u); });
+            q = mul2(q, k);
+            v = mul2(v, mul2(q, q));
         }
-        b = mul2(mul2(w, map2(v, [](float y) { return rsqrt_approx(y); })), x);
+        f2 f = mul2(w, map2(v, [](float y) { return rsqrt_approx(y); }));
+        if constexpr (IG) f = mul2(f, k);
+        b = mul2(f, x);
     } else {
         f2 n;
         sigmoid2(g, a, n);

@@ -21,12 +21,12 @@
 //
 // What bounds it (B200).  fp32 is a stream: 8 x 2048 x 1536 without a rate 49 us, 95 % of the
 // copy rate.  bf16 moves half the bytes and waits: with a rate and an input gate 39 instructions
-// a value forward, of which 19 on the FMA pipe and 4 on the MUFU (52 us for 8 x 2048 x 1536,
-// 60 % of the copy rate), 70 backward (104 us, 54 %); issue is 58 and 52 % busy, no pipe above
+// a value forward, of which 19 on the FMA pipe and 4 on the MUFU (53 us for 8 x 2048 x 1536,
+// 59 % of the copy rate), 70 backward (104 us, 54 %); issue is 58 and 52 % busy, no pipe above
 // 50 %, and the 9.6 warps of an SM spend their time on fixed latencies (0.9 of 2.1 and 1.0 of 2.8
 // stall cycles an instruction) and on memory and the cluster's maps (0.5 and 0.9).  Without rate
 // and input gate 72 and 154 us for 2 x 8192 x 4096 (86 and 71 %).  A few long walks wait for their
-// exchanges: 1 x 131072 x 2048 591 us (56 %).
+// exchanges: 1 x 131072 x 2048 602 us (55 %).
 //
 // Runs of 16 tokens halve the exchanges of runs of 8 (67 against 74 us for the first bf16
 // case); the backward pass would not fit its registers with them.  Maps by st.async instead of

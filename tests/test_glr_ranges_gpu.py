@@ -118,3 +118,21 @@ def test_an_input_gate_of_nan_is_nan_and_one_of_minus_infinity_nothing(L):
     none = S.glr_forward(d["x"] * 0, d["gate"], d["rate"], d["input_gate"], d["h0"])[0]
     assert (y[..., 3] - none[..., 3]).abs().max() <= 1e-30 and torch.isfinite(y[:, 0]).all()
     assert torch.isnan(y[0, 1:, 9]).all()
+
+
+@pytest.mark.parametrize("decay", [False, True])
+@pytest.mark.parametrize("ig", [False, True])
+@pytest.mark.parametrize("L", [1, 3, 20, 400])
+def test_inputs_near_the_largest_number(L, ig, decay):
+    """x close to fp32's largest value is not taken past it on its way to the state."""
+    d = make(1, L, 72, "f32", decay, ig, False, seed=3)
+    r = np.random.default_rng(4)
+    at = torch.from_numpy(r.integers(0, L, 72))
+    d["x"][0, at, torch.arange(72)] = torch.from_numpy((r.choice([-1, 1], 72) * r.uniform(2e38, 3.4e38, 72)).astype(np.float32))
+    if ig:
+        d["input_gate"][:, :, ::2] = 30.0
+    v, c = host(d), cuda(d)
+    y, hf, _ = S.glr_forward(c["x"], c["gate"], c["rate"], c["input_gate"], c["h0"])
+    yr, hr, by, bh = GB.forward(v["x"], v["gate"], v["rate"], v["input_gate"], v["h0"], "f32")
+    close(y, yr, by, "y")
+    close(hf, hr, bh, "h_final")
